@@ -13,7 +13,22 @@ import numpy as np
 from . import _lib
 from ._lib import TlConfig, TlError, TL_FMT_INT4, TL_FMT_BF16, check, lib  # noqa: F401
 
-__all__ = ["TlConfig", "TlError", "LoopedLM", "make_config", "TL_FMT_INT4", "TL_FMT_BF16"]
+__all__ = ["TlConfig", "TlError", "LoopedLM", "make_config", "TL_FMT_INT4", "TL_FMT_BF16", "BatchPlan",
+           "TokenLogprobs", "norm_rope_append", "plan_batch", "rope_table", "token_logprobs", "tree_attention",
+           "tree_attention_workspace"]
+
+_OPS = ("BatchPlan", "TokenLogprobs", "norm_rope_append", "plan_batch", "rope_table", "token_logprobs",
+        "tree_attention", "tree_attention_workspace")
+
+
+def __getattr__(name):
+    """The serving operators (ops.py), imported with their first use: importing the package needs no torch."""
+    if name in _OPS:
+        from . import ops
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 _FMT = {"int4": TL_FMT_INT4, "bf16": TL_FMT_BF16}
 

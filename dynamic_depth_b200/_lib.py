@@ -13,6 +13,8 @@ LIB_PATH = os.path.join(_HERE, "libtl.so")
 
 TL_OK, TL_EINVAL, TL_ENOMEM, TL_ESTATE, TL_EKV, TL_ECUDA, TL_ETIMEOUT, TL_EDEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 TL_FMT_INT4, TL_FMT_BF16 = 0, 1
+TL_F32, TL_F16, TL_BF16 = 0, 1, 2
+TL_BAD_PAGE, TL_BAD_POSITION, TL_BAD_SLOT, TL_TIMED_OUT, TL_BAD_PARENT, TL_BAD_LENGTH = 1, 2, 4, 64, 128, 256
 TL_PROF_NONE, TL_PROF_ATTN, TL_PROF_PROJ, TL_PROF_HEAD = 0, 1, 2, 3
 
 
@@ -25,6 +27,13 @@ class TlConfig(C.Structure):
         ("max_lanes", C.c_int32), ("max_seq", C.c_int32), ("L_max", C.c_int32),
         ("kv_page_tokens", C.c_int32), ("kv_pool_pages", C.c_int32), ("max_prefill_tokens", C.c_int32),
         ("act_split", C.c_int32),
+    ]
+
+
+class TlKvPool(C.Structure):
+    _fields_ = [
+        ("dev_pool", C.c_void_p), ("n_pages", C.c_int64), ("dtype", C.c_int32), ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32), ("page_tokens", C.c_int32),
     ]
 
 
@@ -72,6 +81,21 @@ SIGNATURES = {
     "tl_profile_end": (C.c_int, [C.c_void_p, C.POINTER(C.c_int64), C.POINTER(C.c_double)]),
     "tl_head_argmax_static": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_float, C.c_void_p, C.c_void_p,
                                          C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tl_token_logprobs": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p]),
+    "tl_plan_batch": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p,
+                                C.c_int32, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tl_rope_table": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_double, C.c_void_p]),
+    "tl_norm_rope_append": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p,
+                                      C.c_float, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.POINTER(TlKvPool),
+                                      C.c_void_p, C.c_void_p, C.c_void_p]),
+    "tl_tree_attention": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(TlKvPool), C.c_void_p, C.c_int32, C.c_void_p,
+                                    C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int32,
+                                    C.c_float, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t,
+                                    C.c_void_p, C.c_void_p]),
+    "tl_tree_attention_workspace": (C.c_int, [C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     "tl_read_probe": (C.c_int, [C.c_void_p, C.c_size_t, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p]),
     "tl_stats_get": (C.c_int, [C.c_void_p, C.POINTER(TlStats)]),
     "tl_strerror": (C.c_char_p, [C.c_int]),

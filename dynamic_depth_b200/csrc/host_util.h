@@ -10,6 +10,9 @@ namespace tl {
 // Records the CUDA error text for tl_last_cuda_error() and maps it to a status.
 int check_cuda(cudaError_t e);
 
+// Whether a tl_kv_pool is one that the serving operators take.
+bool kv_pool_ok(const tl_kv_pool* p);
+
 }  // namespace tl
 
 #define TL_CUDA(call)                        \

@@ -1191,6 +1191,13 @@ int encode_all_maps(tl_ctx* c) {
 
 }  // namespace
 
+namespace tl {
+int encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+  return encode_2d(m, dt, base, inner, outer, row_bytes, box_inner, box_outer, sw);
+}
+}  // namespace tl
+
 // ============================================================== C ABI ====
 
 extern "C" int tl_workspace_bytes(const tl_config* cfg, size_t* out) {

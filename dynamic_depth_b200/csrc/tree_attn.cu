@@ -1,0 +1,745 @@
+// Attention of draft trees (and single tokens) over a paged cache.
+//
+// The rows of one request that share a key head (nodes x query heads of the
+// group, node major) are one matrix of queries; its keys are the request's
+// context and its own nodes, read from the pages by TMA in tiles of KT
+// positions.  Work is cut into units of one key tile of one (request, key
+// head, block of BM query rows); the units, in that order, are dealt in equal
+// contiguous ranges to one persistent CTA per SM, so ragged lengths and few
+// long requests fill the machine alike.  A CTA whose range covers all tiles of
+// a row block writes the result; a block cut by range boundaries leaves
+// (max, sum, output) pieces in the workspace - at most two per CTA, whatever
+// the problem - and a second, small kernel joins them in order.  No atomics:
+// results do not depend on timing.
+//
+// Inside a CTA (flash attention, one pass over the keys with a running maximum
+// and sum per row): a producer warp loads tiles into a ring of stages; eight
+// warps multiply, in two groups of four that take alternate tiles, each group
+// split over BM / 16 row blocks and, where those are fewer than four, over
+// parts of the tile's keys.  Every warp keeps its own running state over the
+// keys it sees; the states of a row block meet once per block, in shared
+// memory.
+//
+// Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
+// 4 * hd * BM multiply-adds.
+#include "tree_attn.h"
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "ptx.cuh"
+
+namespace tl {
+
+// Driver entry point of the tensor-map encoder and 2D maps of row-major arrays (runtime.cu).
+int encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+
+namespace tree {
+
+constexpr int kWarps = 8;                     // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD>
+struct Cfg {
+  static constexpr int KT = HD == 128 ? 64 : 128;   // key positions per tile
+  static constexpr int COLS = HD < 64 ? HD : 64;    // columns of a TMA box (one swizzled row)
+  static constexpr int CT = HD / COLS;
+  static constexpr int ROWB = COLS * 2;             // bytes of a box row
+  static constexpr int TILE = KT * ROWB;
+  static constexpr int STAGE = 2 * CT * TILE;       // K boxes, then V boxes
+  static constexpr int STAGES = HD == 32 ? 8 : 5;
+  static constexpr int SLOT = (HD / 2 + 4) * 32;    // floats of one warp's state: output, 2 maxima, 2 sums
+  static constexpr int MERGE = 4 * SLOT * 4;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + MERGE + 256;
+  static_assert(SMEM <= 227 * 1024, "tile ring does not fit");
+};
+
+// Start of each CTA's range, for the joining kernel.
+struct Start {
+  int64_t base;  // first unit of the request that holds the CTA's first unit
+  int64_t total; // units in all
+  int32_t r;
+  int32_t pad;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+struct Req {
+  int32_t row0, n, ctx, len, tiles, blocks;  // blocks: row blocks of a key head
+  bool bad;
+};
+
+template <int KT, int BM>
+__device__ __forceinline__ Req request(const TreeAttnArgs& a, int r) {
+  Req q;
+  const int c0 = a.cu[r], c1 = a.cu[r + 1], ctx = a.ctx[r];
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  q.bad = c0 < 0 || c1 < c0 || c1 > a.n_rows || c1 - c0 > a.max_nodes || ctx < 0 || (int64_t)ctx + (c1 - c0) > cap;
+  q.row0 = c0;
+  q.n = q.bad ? 0 : c1 - c0;
+  q.ctx = ctx;
+  q.len = ctx + q.n;
+  q.tiles = q.len > 0 ? (q.len + KT - 1) / KT : 1;
+  q.blocks = (int)(((int64_t)q.n * (a.H / a.Hk) + BM - 1) / BM);
+  return q;
+}
+
+// A stretch of one row block's key tiles within a CTA's range.
+struct Seg {
+  Req q;
+  int32_t r, hk, blk, t0, t1;
+};
+
+template <int KT, int BM>
+struct Walk {
+  int64_t u, u1, base;
+  int32_t r;
+  Req q;
+  __device__ __forceinline__ bool next(const TreeAttnArgs& a, Seg& s) {
+    if (u >= u1) return false;
+    int64_t units = (int64_t)q.tiles * q.blocks * a.Hk;
+    while (u >= base + units) {
+      base += units;
+      q = request<KT, BM>(a, ++r);
+      units = (int64_t)q.tiles * q.blocks * a.Hk;
+    }
+    const int64_t o = u - base;
+    const int64_t item = o / q.tiles;
+    s.q = q;
+    s.r = r;
+    s.t0 = (int)(o - item * q.tiles);
+    s.t1 = (int)min((int64_t)q.tiles, s.t0 + (u1 - u));
+    s.hk = (int)(item / q.blocks);
+    s.blk = (int)(item - (int64_t)s.hk * q.blocks);
+    u += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// Block-wide: total units, and the request that holds this CTA's first unit.
+template <int KT, int BM>
+__device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_total, Start* sh_start,
+                                           long long* wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long total = 0, u0 = 0, pre = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+      const int r = r0 + threadIdx.x;
+      long long x = 0;
+      if (r < a.R) {
+        const Req q = request<KT, BM>(a, r);
+        x = (long long)q.tiles * q.blocks * a.Hk;
+        if (pass == 0 && q.bad && blockIdx.x == 0 && a.status) atomicOr(a.status, TL_BAD_LENGTH);
+      }
+      const long long mine = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
+      }
+      __syncthreads();
+      if (lane == 31) wsum[warp] = x;
+      __syncthreads();
+      pre = run + x - mine;
+      for (int w = 0; w < kWarps + 1; ++w) {
+        if (w < warp) pre += wsum[w];
+        run += wsum[w];
+      }
+      if (pass == 1 && mine > 0 && u0 >= pre && u0 < pre + mine) *sh_start = Start{pre, total, r, 0};
+    }
+    if (pass == 0) {
+      total = run;
+      u0 = total * blockIdx.x / gridDim.x;
+    }
+  }
+  if (threadIdx.x == 0) *sh_total = total;
+}
+
+template <int HD, int WM, bool BF>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
+  using C = Cfg<HD>;
+  constexpr int KT = C::KT, BM = 16 * WM, WN = 4 / WM, KW = KT / WN, NT = KW / 8;
+  extern __shared__ __align__(1024) uint8_t smem_ta[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_ta) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(merge + 4 * C::SLOT);
+  uint64_t* empty = full + C::STAGES;
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(empty + C::STAGES);  // [STAGES] boxes that landed
+  __shared__ int32_t abort_s;
+  __shared__ int64_t total_s;
+  __shared__ Start start_s;
+  __shared__ long long wsum[kWarps + 1];
+  volatile int32_t* abort_flag = &abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 4);
+    }
+    abort_s = 0;
+    start_s = Start{0, 0, 0, 0};
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  __syncthreads();
+  find_range<KT, BM>(a, &total_s, &start_s, wsum);
+  __syncthreads();
+  const int64_t total = total_s;
+  Walk<KT, BM> walk;
+  walk.u = total * blockIdx.x / gridDim.x;
+  walk.u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int64_t u_first = walk.u;
+  if (threadIdx.x == 0) {
+    Start st = start_s;
+    st.total = total;
+    reinterpret_cast<Start*>(a.ws)[blockIdx.x] = st;
+  }
+  if (walk.u < walk.u1) {
+    walk.base = start_s.base;
+    walk.r = start_s.r;
+    walk.q = request<KT, BM>(a, walk.r);
+    const int P = 1 << a.page_shift;
+    const int PR = P < KT ? P : KT, boxes = KT / PR;  // positions per box, boxes per tile
+    const uint32_t all_boxes = (1u << boxes) - 1u;
+    Seg s;
+    int k = 0;  // tiles of this CTA so far
+    if (warp == kWarps) {
+      // ------------------------------------------------------------ producer
+      bool ok = true;
+      while (ok && walk.next(a, s)) {
+        const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
+        auto page_of = [&](int t) {
+          const int pos = t * KT + lane * PR;
+          return lane < boxes && pos < s.q.len ? __ldg(table + (pos >> a.page_shift)) : -1;
+        };
+        int page = page_of(s.t0);
+        for (int t = s.t0; t < s.t1; ++t, ++k) {
+          const int next_page = t + 1 < s.t1 ? page_of(t + 1) : -1;
+          const int st = k % C::STAGES, round = k / C::STAGES;
+          if (round > 0 && !mbar_wait_warp(smem_u32(&empty[st]), (round - 1) & 1, abort_flag)) { ok = false; break; }
+          const int pos = t * KT + lane * PR;
+          const bool want = lane < boxes && pos < s.q.len;
+          const bool good = want && page >= 0 && page < a.n_pages;
+          if (want && !good && a.status) atomicOr(a.status, TL_BAD_PAGE);
+          const uint32_t in = __ballot_sync(0xffffffffu, good);
+          const uint32_t bar = smem_u32(&full[st]);
+          if (lane == 0) {
+            info[st] = in;
+            mbar_expect_tx(bar, __popc(in) * 2 * C::CT * PR * C::ROWB);
+          }
+          __syncwarp();
+          if (good) {
+            const int64_t y = (((int64_t)page * 2 * a.Hk + s.hk) << a.page_shift) + (pos & (P - 1));
+            const uint32_t dst = smem_u32(ring + st * C::STAGE) + lane * PR * C::ROWB;
+#pragma unroll
+            for (int ct = 0; ct < C::CT; ++ct) {
+              tma_load_2d(dst + ct * C::TILE, &kvmap, ct * 64, (int)y, bar);
+              tma_load_2d(dst + (C::CT + ct) * C::TILE, &kvmap, ct * 64, (int)(y + ((int64_t)a.Hk << a.page_shift)),
+                          bar);
+            }
+          }
+          __syncwarp();
+          page = next_page;
+        }
+      }
+      if (!ok && lane == 0) {  // let the copies in flight land
+        volatile int32_t never = 0;
+        for (int i = k > C::STAGES ? k - C::STAGES : 0; i < k; ++i)
+          mbar_wait(smem_u32(&full[i % C::STAGES]), (i / C::STAGES) & 1, &never);
+      }
+    } else {
+      // ----------------------------------------------------------- consumers
+      const int grp = warp >> 2, wm = (warp & 3) % WM, wn = (warp & 3) / WM;
+      const int part = grp * WN + wn;  // of the 2 WN warps that share a row block
+      const int G = a.H / a.Hk;
+      const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // the thread's rows r0, r0 + 8; columns c0, c0 + 1 of each 8
+      bool ok = true;
+      while (walk.next(a, s)) {
+        const Req& q = s.q;
+        const int rows = q.n * G;
+        int rho[2], node[2];
+        const uint8_t* qp[2];
+        int64_t row[2];
+        int head[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          rho[i] = s.blk * BM + wm * 16 + r0 + 8 * i;
+          const bool in = rho[i] < rows;
+          node[i] = in ? rho[i] / G : -1;
+          head[i] = s.hk * G + (in ? rho[i] - node[i] * G : 0);
+          row[i] = q.row0 + (in ? node[i] : 0);
+          qp[i] = static_cast<const uint8_t*>(a.q) + (row[i] * a.q_stride + (int64_t)head[i] * HD) * 2;
+        }
+        uint32_t qf[HD / 16][4];
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = e & 1, col = kk * 16 + c0 + (e >> 1) * 8;
+            qf[kk][e] = node[i] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp[i] + col * 2)) : 0u;
+          }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float O[HD / 8][4];
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
+
+        for (int t = s.t0; t < s.t1; ++t, ++k) {
+          if ((k & 1) != grp) continue;
+          const int st = k % C::STAGES;
+          if (ok) ok = mbar_wait_warp(smem_u32(&full[st]), (k / C::STAGES) & 1, abort_flag);
+          if (!ok) continue;
+          uint8_t* sk = ring + st * C::STAGE;
+          uint8_t* sv = sk + C::CT * C::TILE;
+          const uint32_t ka = smem_u32(sk), va = smem_u32(sv);
+          const uint32_t landed = info[st];
+          const int key0 = t * KT + wn * KW;  // first position of this warp's part
+          // swizzled address of 16-byte column chunk c of tile row y
+          auto at = [&](uint32_t base, int y, int c) {
+            const int ct = c / (C::COLS / 8), cc = c % (C::COLS / 8);
+            const int sw = C::ROWB == 128 ? (y & 7) : ((y >> 1) & 3);
+            return base + ct * C::TILE + y * C::ROWB + ((cc ^ sw) << 4);
+          };
+          // -------------------------------------------------- S = Q K^T
+          float S[NT][4];
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+              uint32_t b[4];
+              ldsm4(at(ka, wn * KW + j * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, kk * 2 + ((lane >> 3) & 1)), b);
+              mma16816<BF>(S[2 * j], qf[kk], b[0], b[1]);
+              mma16816<BF>(S[2 * j + 1], qf[kk], b[2], b[3]);
+            }
+          // -------------------------------------------------- what each row sees
+          const bool mask = landed != all_boxes || key0 + KW > q.ctx;
+          bool odd_v = false;  // values of the tree hold NaN or infinity
+          if (mask) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int kt = wn * KW + i * 8 + c0 + (e & 1), pos = t * KT + kt, j = pos - q.ctx;
+                bool see = pos < q.len && (landed >> (kt / PR) & 1u);
+                if (see && j >= 0) {
+                  const int nd = node[e >> 1];
+                  see = nd >= 0 && (a.masks ? j < 32 * a.words &&
+                                                  (__ldg(a.masks + row[e >> 1] * a.words + (j >> 5)) >> (j & 31) & 1u)
+                                            : j <= nd);
+                }
+                if (!see) S[i][e] = -INFINITY;
+              }
+            // values of positions that nobody sees may be anything: 0 * NaN is not 0
+            const bool scan = q.n > 1 || a.masks;
+            for (int i = lane; i < KW * (HD / 8); i += 32) {
+              const int y = wn * KW + i / (HD / 8), pos = t * KT + y;
+              uint4* p = reinterpret_cast<uint4*>(sv + (at(va, y, i % (HD / 8)) - va));
+              if (pos >= q.len || !(landed >> (y / PR) & 1u)) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else if (scan && pos >= q.ctx) {
+                constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
+                const uint4 w = *p;
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd_v |= (u[e] & X) == X || (u[e] >> 16 & X) == X;
+              }
+            }
+            odd_v = __any_sync(0xffffffffu, odd_v);  // orders the zeros before the reads below, too
+            __syncwarp();
+          }
+          // -------------------------------------------------- running maximum and sum
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            mx[0] = fmaxf(mx[0], fmaxf(S[i][0], S[i][1]));
+            mx[1] = fmaxf(mx[1], fmaxf(S[i][2], S[i][3]));
+          }
+          float mb[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            const float mn = fmaxf(m[i], mx[i] * a.scale_log2);
+            mb[i] = mn == -INFINITY ? 0.f : mn;
+            const float corr = ex2(m[i] - mb[i]);  // 0 from -inf
+            l[i] *= corr;
+            if (mn != m[i]) {
+#pragma unroll
+              for (int d = 0; d < HD / 8; ++d) { O[d][2 * i] *= corr; O[d][2 * i + 1] *= corr; }
+            }
+            m[i] = mn;
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              S[i][e] = ex2(fmaf(S[i][e], a.scale_log2, -mb[e >> 1]));
+              l[e >> 1] += S[i][e];
+            }
+          // -------------------------------------------------- O += P V
+          if (!odd_v) {
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+              // one rounding of each probability to the values' type (the matrix instruction takes one type)
+              const uint32_t p[4] = {pack2<BF>(S[2 * j][0], S[2 * j][1]), pack2<BF>(S[2 * j][2], S[2 * j][3]),
+                                     pack2<BF>(S[2 * j + 1][0], S[2 * j + 1][1]),
+                                     pack2<BF>(S[2 * j + 1][2], S[2 * j + 1][3])};
+#pragma unroll
+              for (int d = 0; d < HD / 16; ++d) {
+                uint32_t b[4];
+                ldsm4t(at(va, wn * KW + j * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, d * 2 + ((lane >> 4) & 1)), b);
+                mma16816<BF>(O[2 * d], p, b[0], b[1]);
+                mma16816<BF>(O[2 * d + 1], p, b[2], b[3]);
+              }
+            }
+          } else {
+            // a value that some row does not see is not finite: products by hand, where the row sees the key
+            float pl[NT * 4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pl[i * 4 + e] = S[i][e];
+#pragma unroll 1
+            for (int y = 0; y < KW; ++y) {
+              const int src = (lane & ~3) | ((y & 7) >> 1), e = y & 1;
+              const float p0 = __shfl_sync(0xffffffffu, pl[(y >> 3) * 4 + e], src);
+              const float p1 = __shfl_sync(0xffffffffu, pl[(y >> 3) * 4 + 2 + e], src);
+#pragma unroll
+              for (int d = 0; d < HD / 8; ++d) {
+                const float2 v = unpack2<BF>(*reinterpret_cast<const uint32_t*>(
+                    sv + (at(va, wn * KW + y, d) - va) + c0 * 2));
+                if (p0 != 0.f) { O[d][0] = fmaf(p0, v.x, O[d][0]); O[d][1] = fmaf(p0, v.y, O[d][1]); }
+                if (p1 != 0.f) { O[d][2] = fmaf(p1, v.x, O[d][2]); O[d][3] = fmaf(p1, v.y, O[d][3]); }
+              }
+            }
+          }
+          if (mask) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the stage's next copy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+        }
+
+        // ---------------------------------------- the states of a row block meet
+#pragma unroll
+        for (int half = WN; half >= 1; half >>= 1) {
+          if (part >= half && part < 2 * half) {
+            float* b = merge + (wm * half + part - half) * C::SLOT + lane;
+#pragma unroll
+            for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[(d * 4 + e) * 32] = O[d][e];
+            b[(HD / 2) * 32] = m[0];
+            b[(HD / 2 + 1) * 32] = m[1];
+            b[(HD / 2 + 2) * 32] = l[0];
+            b[(HD / 2 + 3) * 32] = l[1];
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+          if (part < half) {
+            const float* b = merge + (wm * half + part) * C::SLOT + lane;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float m2 = b[(HD / 2 + i) * 32], mn = fmaxf(m[i], m2);
+              const float z = mn == -INFINITY ? 0.f : mn;
+              const float x = ex2(m[i] - z), y = ex2(m2 - z);
+              l[i] = l[i] * x + b[(HD / 2 + 2 + i) * 32] * y;
+              m[i] = mn;
+              // a state that saw nothing adds nothing, whatever the other holds
+#pragma unroll
+              for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  O[d][2 * i + e] = O[d][2 * i + e] * x + b[(d * 4 + 2 * i + e) * 32] * y;
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        }
+        if (part == 0 && ok) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+          }
+          const bool whole = s.t0 == 0 && s.t1 == q.tiles;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (node[i] < 0) continue;
+              const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+              const int64_t o = row[i] * a.out_stride + (int64_t)head[i] * HD + c0;
+#pragma unroll
+              for (int d = 0; d < HD / 8; ++d) {
+                const float x = O[d][2 * i] * inv, y = O[d][2 * i + 1] * inv;
+                if (a.out_f32)
+                  *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + d * 8) = make_float2(x, y);
+                else
+                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + d * 8) = pack2<BF>(x, y);
+                if (a.out16) {
+                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + c0, x, a.split16);
+                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + c0 + 1, y, a.split16);
+                }
+              }
+              if (a.lse && (lane & 3) == 0)
+                a.lse[row[i] * a.H + head[i]] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+            }
+          } else {
+            // slot 0: the CTA's first stretch, when it does not begin the row block; slot 1: the last
+            const int64_t begin = walk.u - (s.t1 - s.t0);
+            const int slot = begin == u_first && s.t0 > 0 ? 0 : 1;
+            float* ws = reinterpret_cast<float*>(a.ws + gridDim.x * sizeof(Start)) +
+                        ((int64_t)blockIdx.x * 2 + slot) * BM * (HD + 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float* w = ws + (wm * 16 + r0 + 8 * i) * (HD + 2);
+              if ((lane & 3) == 0) *reinterpret_cast<float2*>(w) = make_float2(m[i], l[i]);
+#pragma unroll
+              for (int d = 0; d < HD / 8; ++d)
+                *reinterpret_cast<float2*>(w + 2 + d * 8 + c0) = make_float2(O[d][2 * i], O[d][2 * i + 1]);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_s && a.status) atomicOr(a.status, TL_TIMED_OUT);
+}
+
+// Joins the pieces of the row blocks that the CTAs' ranges cut: CTA b looks at
+// the cut at the start of range b, and acts if it is the first of its block.
+// blockIdx.y: 4 rows of the block.
+template <int HD, int BM, bool BF>
+__global__ void __launch_bounds__(128) join_kernel(const TreeAttnArgs a) {
+  constexpr int KT = Cfg<HD>::KT;
+  pdl_wait();
+  const int G = gridDim.x, b = blockIdx.x;
+  const Start st = reinterpret_cast<const Start*>(a.ws)[b];
+  const int64_t U = st.total;
+  auto first = [&](int64_t c) { return U * c / G; };
+  auto owner = [&](int64_t u) { return (int)(((u + 1) * G - 1) / U); };
+  const int64_t u = first(b);
+  if (b == 0 || u >= first(b + 1)) return;  // an empty range has no cut of its own
+  const Req q = request<KT, BM>(a, st.r);
+  const int64_t item = (u - st.base) / q.tiles, ua = st.base + item * q.tiles, ub = ua + q.tiles;
+  if (u == ua || owner(ua) != owner(u - 1)) return;
+  const int hk = (int)(item / q.blocks), blk = (int)(item - (int64_t)hk * q.blocks), grp = a.H / a.Hk;
+  const int rr = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int y = blockIdx.y * 4 + rr, rho = blk * BM + y;
+  if (rho >= q.n * grp) return;
+  const float* ws = reinterpret_cast<const float*>(a.ws + G * sizeof(Start));
+  float m = -INFINITY, l = 0.f, O[HD / 32];
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) O[e] = 0.f;
+  for (int c = owner(ua); c < G;) {
+    const float* w = ws + ((int64_t)c * 2 + (ua < first(c) ? 0 : 1)) * BM * (HD + 2) + y * (HD + 2);
+    const float m2 = w[0], l2 = w[1], mn = fmaxf(m, m2), z = mn == -INFINITY ? 0.f : mn;
+    const float x = ex2(m - z), x2 = ex2(m2 - z);
+    l = l * x + l2 * x2;
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e) O[e] = O[e] * x + w[2 + e * 32 + lane] * x2;
+    m = mn;
+    if (first(c + 1) >= ub) break;
+    c = owner(first(c + 1));
+  }
+  const int node = rho / grp, head = hk * grp + rho - node * grp;
+  const int64_t row = q.row0 + node;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) {
+    const float v = O[e] * inv;
+    const int64_t o = row * a.out_stride + (int64_t)head * HD + e * 32 + lane;
+    if (a.out_f32) static_cast<float*>(a.out)[o] = v;
+    else if constexpr (BF) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(a.out)[o] = __float2half_rn(v);
+    if (a.out16) act16_put(a.out16, row, a.H * HD, head * HD + e * 32 + lane, v, a.split16);
+  }
+  if (a.lse && lane == 0) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+static int block_rows(int64_t rows_per_head) { return rows_per_head <= 16 ? 16 : rows_per_head <= 32 ? 32 : 64; }
+
+template <int HD, int WM, bool BF>
+static int launch(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cudaStream_t s) {
+  auto kern = attn_kernel<HD, WM, BF>;
+  TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM));
+  kern<<<n_sms, kThreads, Cfg<HD>::SMEM, s>>>(map, a);
+  TL_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(n_sms, 16 * WM / 4);
+  lc.blockDim = dim3(128);
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  TL_CUDA(cudaLaunchKernelEx(&lc, join_kernel<HD, 16 * WM, BF>, a));
+  return check_cuda(cudaGetLastError());
+}
+
+template <int HD, bool BF>
+static int launch_rows(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cudaStream_t s) {
+  switch (block_rows((int64_t)a.max_nodes * (a.H / a.Hk))) {
+    case 16: return launch<HD, 1, BF>(a, map, n_sms, s);
+    case 32: return launch<HD, 2, BF>(a, map, n_sms, s);
+    default: return launch<HD, 4, BF>(a, map, n_sms, s);
+  }
+}
+
+template <int HD>
+static int run(const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms, cudaStream_t s) {
+  using C = Cfg<HD>;
+  CUtensorMap map;
+  const bool bf = p.dtype == TL_BF16;
+  const uint64_t rows = (uint64_t)p.n_pages * 2 * p.n_kv_heads * p.page_tokens;
+  TL_TRY(encode_map_2d(&map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.dev_pool, HD,
+                       rows, HD * 2, C::COLS, p.page_tokens < C::KT ? p.page_tokens : C::KT,
+                       C::ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+  return bf ? launch_rows<HD, true>(a, map, n_sms, s) : launch_rows<HD, false>(a, map, n_sms, s);
+}
+
+static int sm_count(int* n) {
+  int dev = 0;
+  TL_CUDA(cudaGetDevice(&dev));
+  TL_CUDA(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev));
+  return TL_OK;
+}
+
+}  // namespace tree
+
+size_t tree_attn_workspace(int hd, int64_t rows_per_head, int n_sms) {
+  return (size_t)n_sms * sizeof(tree::Start) + (size_t)n_sms * 2 * tree::block_rows(rows_per_head) * (hd + 2) * 4;
+}
+
+int tree_attn_run(TreeAttnArgs a, const tl_kv_pool& p, cudaStream_t s, int64_t* launches) {
+  int n_sms = 0;
+  TL_TRY(tree::sm_count(&n_sms));
+  a.Hk = p.n_kv_heads;
+  a.n_pages = p.n_pages;
+  a.page_shift = 0;
+  while ((1 << a.page_shift) < p.page_tokens) ++a.page_shift;
+  if (launches) *launches += 2;
+  switch (p.head_dim) {
+    case 32: return tree::run<32>(a, p, n_sms, s);
+    case 64: return tree::run<64>(a, p, n_sms, s);
+    default: return tree::run<128>(a, p, n_sms, s);
+  }
+}
+
+}  // namespace tl
+
+using namespace tl;
+
+extern "C" int tl_tree_attention_workspace(int32_t head_dim, int32_t n_heads, int32_t n_kv_heads, int32_t max_nodes,
+                                           size_t* out_bytes) {
+  if (!out_bytes || (head_dim != 32 && head_dim != 64 && head_dim != 128) || n_heads < 1 || n_kv_heads < 1 ||
+      n_heads % n_kv_heads || max_nodes < 1)
+    return TL_EINVAL;
+  int n_sms = 0;
+  TL_TRY(tree::sm_count(&n_sms));
+  *out_bytes = tree_attn_workspace(head_dim, (int64_t)max_nodes * (n_heads / n_kv_heads), n_sms);
+  return TL_OK;
+}
+
+extern "C" int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_kv_pool* pool,
+                                 const int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_ctx,
+                                 const int32_t* dev_cu, int32_t R, int32_t n_rows, int32_t n_heads, int32_t max_nodes,
+                                 const uint32_t* dev_masks, int32_t mask_words, float scale, void* dev_out,
+                                 int32_t out_dtype, int64_t out_stride, float* dev_lse, void* dev_workspace,
+                                 size_t workspace_bytes, int32_t* dev_status, void* cuda_stream) {
+  if (!kv_pool_ok(pool)) return TL_EINVAL;
+  const int64_t width = (int64_t)n_heads * pool->head_dim;
+  const int os = out_dtype == TL_F32 ? 4 : 2;
+  if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || n_rows < 0 || max_pages < 1 || max_nodes < 1 ||
+      (out_dtype != TL_F32 && out_dtype != pool->dtype) || (n_rows > 1 && (q_stride < width || out_stride < width)) ||
+      (q_stride * 2) % 16 || (out_stride * os) % 16 || (dev_masks != nullptr) != (mask_words > 0) || mask_words < 0 ||
+      (dev_masks && max_nodes > 32 * (int64_t)mask_words) || !(scale >= 0.f) || scale > 3e38f ||
+      (int64_t)max_nodes * (n_heads / pool->n_kv_heads) > 0x7fffffff)
+    return TL_EINVAL;
+  if (R == 0 || n_rows == 0) return TL_OK;
+  if (!dev_q || !dev_block_table || !dev_ctx || !dev_cu || !dev_out || !dev_workspace) return TL_EINVAL;
+  if (((uintptr_t)dev_q & 15) || ((uintptr_t)dev_out & 15) || ((uintptr_t)dev_block_table & 3) ||
+      ((uintptr_t)dev_ctx & 3) || ((uintptr_t)dev_cu & 3) || ((uintptr_t)dev_masks & 3) || ((uintptr_t)dev_lse & 3) ||
+      ((uintptr_t)dev_workspace & 255) || ((uintptr_t)dev_status & 3))
+    return TL_EINVAL;
+  size_t need = 0;
+  TL_TRY(tl_tree_attention_workspace(pool->head_dim, n_heads, pool->n_kv_heads, max_nodes, &need));
+  if (workspace_bytes < need) return TL_ENOMEM;
+  if (scale == 0.f) scale = 1.f / sqrtf((float)pool->head_dim);
+  TreeAttnArgs a{};
+  a.q = dev_q;
+  a.q_stride = q_stride;
+  a.table = dev_block_table;
+  a.max_pages = max_pages;
+  a.ctx = dev_ctx;
+  a.cu = dev_cu;
+  a.R = R;
+  a.n_rows = n_rows;
+  a.H = n_heads;
+  a.max_nodes = max_nodes;
+  a.masks = dev_masks;
+  a.words = mask_words;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.out = dev_out;
+  a.out_f32 = out_dtype == TL_F32;
+  a.out_stride = out_stride;
+  a.lse = dev_lse;
+  a.ws = static_cast<char*>(dev_workspace);
+  a.status = dev_status;
+  return tree_attn_run(a, *pool, (cudaStream_t)cuda_stream);
+}

@@ -1,0 +1,218 @@
+"""Serving operators over a caller-owned paged cache (include/tl.h, "serving operators").
+
+Marshalling only: shapes, types and strides are checked here, everything else by the library.  Every call runs on
+the current stream of its tensors' device and allocates only its outputs (and a workspace where none is given).
+
+The cache is one tensor of pages, [n_pages, 2 (keys, values), kv heads, page tokens, head width], fp16 or bf16.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._lib import TL_BF16, TL_F16, TL_F32, TlKvPool, check, lib
+
+_DT = {torch.float32: TL_F32, torch.float16: TL_F16, torch.bfloat16: TL_BF16}
+
+
+class TokenLogprobs(NamedTuple):
+    """Outputs of token_logprobs, one row per row of logits (None where not asked for)."""
+    logprob: Optional[torch.Tensor]
+    rank: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_ids: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+
+
+class BatchPlan(NamedTuple):
+    """Outputs of plan_batch (the block table is extended in place)."""
+    cu: torch.Tensor
+    lens: torch.Tensor
+    granted: torch.Tensor
+    free_head: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    masks: Optional[torch.Tensor]
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _flat(t, dtype, n, name, device):
+    """A contiguous device vector of n elements (None passes as a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements on {device} is wanted")
+    return t.data_ptr()
+
+
+class _on:
+    """The device of a call made current, where it is not; .stream is its current stream."""
+
+    def __init__(self, device):
+        _need(device.type == "cuda", "the tensors must be on a CUDA device")
+        self.guard = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard:
+            self.guard.__exit__(*exc)
+
+
+def _pool(pool) -> TlKvPool:
+    _need(pool.dim() == 5 and pool.shape[1] == 2 and pool.is_contiguous() and pool.dtype in _DT,
+          "pool: a contiguous [pages, 2, kv heads, page tokens, head width] tensor of fp16 or bf16 is wanted")
+    n, _, h, p, d = pool.shape
+    return TlKvPool(pool.data_ptr(), n, _DT[pool.dtype], h, d, p)
+
+
+def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
+    """Log probability and rank of each row's target, entropy, log-sum-exp and the n_top best tokens of logits
+    [rows, vocab] (fp32, fp16 or bf16; rows may be strided).  targets int32 [rows], -1 for none."""
+    _need(logits.dim() == 2 and logits.dtype in _DT and (logits.shape[1] <= 1 or logits.stride(1) == 1),
+          "logits: [rows, vocab] of fp32, fp16 or bf16 with adjacent columns is wanted")
+    rows, vocab = logits.shape
+    dev = logits.device
+    tp = _flat(targets, torch.int32, rows, "targets", dev)
+    with _on(dev) as stream:
+        f = torch.empty((3, rows), dtype=torch.float32, device=dev)
+        lp, ent, lse = f.unbind(0)
+        rank = torch.empty(rows, dtype=torch.int32, device=dev) if targets is not None else None
+        ids = torch.empty((rows, n_top), dtype=torch.int32, device=dev) if n_top else None
+        top = torch.empty((rows, n_top), dtype=torch.float32, device=dev) if n_top else None
+        check(lib().tl_token_logprobs(
+            logits.data_ptr(), _DT[logits.dtype], rows, vocab, logits.stride(0) if rows > 1 else vocab, tp, n_top,
+            lp.data_ptr() if tp is not None else None, rank.data_ptr() if rank is not None else None, ent.data_ptr(),
+            lse.data_ptr(), ids.data_ptr() if n_top else None, top.data_ptr() if n_top else None, stream),
+            "tl_token_logprobs")
+    return TokenLogprobs(lp if targets is not None else None, rank, ent, lse, ids, top)
+
+
+def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: int, n_rows: int, parents=None,
+               mask_words: int = 0, status=None) -> BatchPlan:
+    """Row offsets, slots, positions and tree masks of a batch's new tokens from the request lengths; the block table
+    [R, max_pages] (int32) gets the pages granted from free_pages[free_head[0]:].  n_rows: rows of the row outputs
+    (at least the sum of fresh; rows past that sum are not written)."""
+    R = cached.numel()
+    dev = cached.device
+    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32
+          and block_table.is_contiguous() and block_table.device == dev,
+          "block_table: a contiguous int32 [R, max_pages] tensor is wanted")
+    _need(free_pages.dim() == 1, "free_pages: a vector is wanted")
+    i32 = torch.int32
+    args = (_flat(cached, i32, R, "cached", dev), _flat(fresh, i32, R, "fresh", dev), R, page_tokens,
+            block_table.data_ptr(), block_table.shape[1],
+            _flat(free_pages, i32, free_pages.numel(), "free_pages", dev), free_pages.numel(),
+            _flat(free_head, i32, 1, "free_head", dev), _flat(parents, i32, n_rows, "parents", dev), n_rows,
+            mask_words)
+    st = _flat(status, i32, 1, "status", dev)
+    _need(0 <= mask_words <= 8 and n_rows >= 0, "mask_words 0 .. 8, n_rows >= 0")
+    with _on(dev) as stream:
+        small = torch.empty(3 * R + 2, dtype=i32, device=dev)
+        cu, lens, granted, head = small[:R + 1], small[R + 1:2 * R + 1], small[2 * R + 1:3 * R + 1], small[3 * R + 1:]
+        slots = torch.empty(n_rows, dtype=torch.int64, device=dev)
+        pos = torch.empty(n_rows, dtype=i32, device=dev)
+        masks = torch.empty((n_rows, mask_words), dtype=i32, device=dev) if mask_words else None
+        at = small.data_ptr()
+        # an empty tensor has no address; the library wants one where a mask is asked for
+        mp = None if masks is None else (masks.data_ptr() or at)
+        check(lib().tl_plan_batch(*args, at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (3 * R + 1),
+                                  slots.data_ptr(), pos.data_ptr(), mp, st, stream), "tl_plan_batch")
+    return BatchPlan(cu, lens, granted, head, slots, pos, masks)
+
+
+def rope_table(length: int, head_dim: int, base: float = 1e4, device="cuda") -> torch.Tensor:
+    """(cos, sin) of position * base^(-2i / head_dim): fp32 [length, head_dim / 2, 2], angles in fp64."""
+    dev = torch.device(device)
+    with _on(dev) as stream:
+        t = torch.empty((length, head_dim // 2, 2), dtype=torch.float32, device=dev)
+        check(lib().tl_rope_table(t.data_ptr(), length, head_dim, float(base), stream), "tl_rope_table")
+    return t
+
+
+def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=None, k_gain=None, eps: float = 1e-6,
+                     q_out=None, status=None) -> torch.Tensor:
+    """Per-head RMSNorm (with gains) and rotation of the queries and keys of qkv [rows, (q | k | v) heads * width],
+    keys and values stored at `slots` of the pool; returns the queries [rows, n_heads, width] in the pool's type."""
+    p = _pool(pool)
+    dev, rows, hd = pool.device, qkv.shape[0], p.head_dim
+    _need(qkv.dim() == 2 and qkv.dtype in _DT and qkv.shape[1] == (n_heads + 2 * p.n_kv_heads) * hd
+          and qkv.stride(1) == 1 and qkv.device == dev, "qkv: [rows, (q + 2 kv heads) * width] of the pool's device")
+    _need(rope.dim() == 3 and rope.shape[1:] == (hd // 2, 2), "rope: a rope_table of the pool's head width is wanted")
+    i32, f32 = torch.int32, torch.float32
+    sp = _flat(slots, torch.int64, rows, "slots", dev)
+    pp = _flat(positions, i32, rows, "positions", dev)
+    rp = _flat(rope, f32, rope.numel(), "rope", dev)
+    gq, gk = _flat(q_gain, f32, hd, "q_gain", dev), _flat(k_gain, f32, hd, "k_gain", dev)
+    st = _flat(status, i32, 1, "status", dev)
+    with _on(dev) as stream:
+        if q_out is None:
+            q_out = torch.empty((rows, n_heads, hd), dtype=pool.dtype, device=dev)
+        qp = _flat(q_out, pool.dtype, rows * n_heads * hd, "q_out", dev)
+        check(lib().tl_norm_rope_append(qkv.data_ptr(), _DT[qkv.dtype], rows,
+                                        qkv.stride(0) if rows > 1 else qkv.shape[1], n_heads, gq, gk, eps, rp,
+                                        rope.shape[0], pp, sp, C.byref(p), qp, st, stream), "tl_norm_rope_append")
+    return q_out
+
+
+def tree_attention_workspace(head_dim: int, n_heads: int, n_kv_heads: int, max_nodes: int, device="cuda"):
+    """A workspace for tree_attention calls of these sizes (one per call that may run at the same time)."""
+    n = C.c_size_t()
+    dev = torch.device(device)
+    with _on(dev):
+        check(lib().tl_tree_attention_workspace(head_dim, n_heads, n_kv_heads, max_nodes, C.byref(n)),
+              "tl_tree_attention_workspace")
+        return torch.empty(n.value, dtype=torch.uint8, device=dev)
+
+
+def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=None, scale: float = 0.0, out=None,
+                   return_lse: bool = False, workspace=None, status=None):
+    """Attention of draft trees over the pool's pages: rows cu[r] .. cu[r+1] of q [rows, heads, width] see request r's
+    first ctx_lens[r] positions and the nodes behind them that their mask words name (None: the earlier nodes and
+    themselves).  out: a given tensor's type (the pool's or fp32), else the pool's.  Returns out, or (out, lse)."""
+    p = _pool(pool)
+    dev, hd = pool.device, p.head_dim
+    _need(q.dim() == 3 and q.dtype == pool.dtype and q.shape[2] == hd and q.stride(2) == 1 and q.stride(1) == hd
+          and q.device == dev, "q: [rows, heads, width] of the pool's type, heads adjacent")
+    rows, H = q.shape[0], q.shape[1]
+    R = ctx_lens.numel()
+    i32 = torch.int32
+    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == i32
+          and block_table.is_contiguous() and block_table.device == dev,
+          "block_table: a contiguous int32 [R, max_pages] tensor is wanted")
+    cp, up = _flat(ctx_lens, i32, R, "ctx_lens", dev), _flat(cu, i32, R + 1, "cu", dev)
+    words = 0
+    if masks is not None:
+        _need(masks.dim() == 2 and masks.shape[0] == rows, "masks: int32 [rows, words] is wanted")
+        words = masks.shape[1]
+    mp = _flat(masks, i32, rows * words, "masks", dev)
+    st = _flat(status, i32, 1, "status", dev)
+    with _on(dev) as stream:
+        if out is None:
+            out = torch.empty((rows, H, hd), dtype=q.dtype, device=dev)
+        _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1 and out.stride(1) == hd
+              and out.device == dev, "out: the shape of q, heads adjacent")
+        lse = torch.empty((rows, H), dtype=torch.float32, device=dev) if return_lse else None
+        if workspace is None:
+            n = C.c_size_t()
+            check(lib().tl_tree_attention_workspace(hd, H, p.n_kv_heads, max_nodes, C.byref(n)),
+                  "tl_tree_attention_workspace")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        check(lib().tl_tree_attention(
+            q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
+            block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
+            out.stride(0) if rows > 1 else H * hd, lse.data_ptr() if return_lse else None, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st, stream), "tl_tree_attention")
+    return (out, lse) if return_lse else out

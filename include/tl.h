@@ -460,6 +460,173 @@ int tl_head_argmax_static(const float* dev_h, int32_t rows, const float* dev_g_f
                           const uint8_t* dev_head_packed, const uint16_t* dev_head_scales, int32_t V,
                           int32_t d, int32_t group, float* dev_logits, int32_t* dev_argmax, void* cuda_stream);
 
+/* ------------------------------------------------- serving operators -- */
+
+/* Operators for programs that keep their own paged cache and drive their own
+ * batches (the context's calls above keep theirs inside the workspace):
+ * tl_plan_batch finds pages, slots, positions and tree masks for the new
+ * tokens of a batch, tl_norm_rope_append fills the slots, tl_tree_attention
+ * attends, tl_token_logprobs reads the head's logits.  tl_speculate_tree and
+ * tl_score run them on a context's cache and logits.
+ *
+ * Each call enqueues on cuda_stream, which must belong to the current device,
+ * and waits for nothing; all pointers are device pointers; none allocates, so
+ * every call can be captured into a CUDA graph.  Arguments the host can check
+ * give TL_EINVAL (or TL_ENOMEM for a workspace that is too small) with nothing
+ * enqueued.  What only the device sees (a page id, a slot, a length) is
+ * checked there: the access is skipped and a bit is set in *dev_status, an
+ * int32 that the caller clears and reads (NULL: not reported). */
+typedef enum tl_dtype { TL_F32 = 0, TL_F16 = 1, TL_BF16 = 2 } tl_dtype;
+
+enum {
+    TL_BAD_PAGE = 1,      /* page id outside the pool                           */
+    TL_BAD_POSITION = 2,  /* position outside the rotation table                */
+    TL_BAD_SLOT = 4,      /* slot outside the pool                              */
+    TL_TIMED_OUT = 64,    /* a bounded device wait ran out; the outputs are void */
+    TL_BAD_PARENT = 128,  /* a tree node's parent is not an earlier node        */
+    TL_BAD_LENGTH = 256   /* a length is negative or past its table, mask or rows */
+};
+
+/* A pool of cache pages in the context's page layout: page i holds
+ * page_tokens positions as keys [n_kv_heads][page_tokens][head_dim] followed by
+ * values of the same shape.  dtype TL_F16 or TL_BF16; head_dim 32, 64 or 128;
+ * page_tokens a power of two from 16 to 1024; dev_pool 16-byte aligned;
+ * n_pages * 2 * n_kv_heads * page_tokens < 2^31 (bytes are not limited by it). */
+typedef struct tl_kv_pool {
+    void* dev_pool;
+    int64_t n_pages;
+    int32_t dtype;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+} tl_kv_pool;
+
+/* Log probability, rank, entropy and best alternatives of each row of logits
+ * x[0 .. vocab), with lse = ln sum_i exp(x_i):
+ *   dev_logprob[r] = x_t - lse for the token t = dev_targets[r];
+ *   dev_rank[r]    = tokens placed before t (larger logit, or the same logit
+ *                    and a lower id);
+ *   dev_entropy[r] = lse - sum_i p_i x_i;      dev_lse[r] = lse;
+ *   dev_top_ids / dev_top_logprobs [rows][n_top]: the n_top first tokens in
+ *                    that order and their log probabilities.
+ * A target of -1 means none: logprob 0, rank -1; any other target outside the
+ * vocabulary gives NaN and -1.  A logit of -infinity is a token that cannot
+ * be: p = 0, no part of the entropy.  Rows of -infinity alone have lse and
+ * log probabilities -infinity and entropy 0.  In a row that holds +infinity or
+ * NaN every floating output is NaN; the order places NaN before every number
+ * (and lower ids first, as among equals), and the rank is -1 where there is a
+ * NaN.  -0 equals +0.
+ *   dev_logits: [rows] rows of vocab elements of dtype, row_stride elements
+ *     apart, row_stride >= vocab or rows == 1, aligned to the element size;
+ *   vocab 1 .. 2^20; 0 <= n_top <= 64 and <= vocab; rows may be 0;
+ *   outputs: NULL where not wanted (dev_logprob and dev_rank need dev_targets;
+ *     both top outputs need n_top > 0). */
+int tl_token_logprobs(const void* dev_logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t row_stride,
+                      const int32_t* dev_targets, int32_t n_top, float* dev_logprob, int32_t* dev_rank,
+                      float* dev_entropy, float* dev_lse, int32_t* dev_top_ids, float* dev_top_logprobs,
+                      void* cuda_stream);
+
+/* Pages, slots and positions of a batch's new tokens, from the request
+ * lengths, on the device.  Request r holds dev_cached[r] tokens in the cache
+ * and adds dev_fresh[r]; row i of the batch is new token j of request r with
+ * i = cu[r] + j.
+ *   dev_cu [R + 1]: prefix sums of dev_fresh (the batch's row offsets);
+ *   dev_block_table [R][max_pages]: in, the pages each request holds
+ *     (ceil(cached / page_tokens) entries); out, followed by the pages it was
+ *     granted.  Other entries are left as they are;
+ *   dev_free_pages [n_free]: free page ids, taken from index *dev_free_head
+ *     on, request after request;  *dev_free_head_out: the next index;
+ *   dev_granted [R]: 1 where the request's new tokens have pages.  A request
+ *     is granted when it needs no page, or when the list holds the pages that
+ *     it and every request before it need; never past max_pages;
+ *   dev_lens [R]: cached + fresh where granted, cached elsewhere;
+ *   dev_slots [n_rows] int64: page * page_tokens + offset; -1 in a request that
+ *     was refused;
+ *   dev_positions [n_rows]: cached + j, or in a tree cached + depth of the node;
+ *   dev_masks [n_rows][mask_words]: bit j of a row's words is set where the row
+ *     sees new token j of its request: its ancestors and itself.
+ * dev_parents [n_rows]: NULL, each request's new tokens follow one another; or
+ * trees: the parent of each new token as an index among its request's new
+ * tokens, -1 for one that follows the cache; a parent comes before its child
+ * (else TL_BAD_PARENT and it counts as -1).  dev_parents needs mask_words > 0
+ * or NULL masks.  Tokens beyond 32 * mask_words of a request have no bit, their
+ * own rows included (TL_BAD_LENGTH).
+ * n_rows: rows the row outputs hold; rows from cu[R] on are left as they are,
+ * rows past n_rows are not written (TL_BAD_LENGTH).  A negative length, or a
+ * dev_fresh above 2^24, counts as 0 and is refused (TL_BAD_LENGTH).
+ * 1 <= R <= 8192; page_tokens a power of two, 1 .. 4096; mask_words 0 .. 8;
+ * dev_free_head_out must not be dev_free_head, nor dev_lens dev_cached.
+ * NULL allowed: dev_parents, dev_masks (mask_words 0), dev_status. */
+int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
+                  int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages, int32_t n_free,
+                  const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows, int32_t mask_words,
+                  int32_t* dev_cu, int32_t* dev_lens, int32_t* dev_granted, int32_t* dev_free_head_out,
+                  int64_t* dev_slots, int32_t* dev_positions, uint32_t* dev_masks, int32_t* dev_status,
+                  void* cuda_stream);
+
+/* Rotation table: dev_table fp32 [length][head_dim / 2][2] = (cos, sin) of
+ * position * base^(-2i / head_dim), angles in fp64. */
+int tl_rope_table(float* dev_table, int32_t length, int32_t head_dim, double base, void* cuda_stream);
+
+/* Queries, keys and values of a batch's rows in one pass: each query and key
+ * head is RMS-normalised over head_dim (x * rsqrt(mean x^2 + eps) * gain; NULL
+ * gains: not normalised), rotated in pairs (i, i + head_dim/2) by the table's
+ * row of its position, and rounded once to the cache's type; queries go to
+ * dev_q_out, keys and values (values only rounded) to the row's slot of the
+ * pool.
+ *   dev_qkv: rows of [n_heads q | n_kv_heads k | n_kv_heads v] heads, dtype
+ *     TL_F32, TL_F16 or TL_BF16, row_stride elements apart; 16-byte aligned
+ *     rows;
+ *   dev_q_gain / dev_k_gain: fp32 [head_dim], both or neither;
+ *   dev_table: tl_rope_table's layout, `length` positions; dev_positions int32;
+ *   dev_slots: int64, as from tl_plan_batch; -1: the row's keys and values are
+ *     not stored.  Two rows with the same slot leave either's values there;
+ *   dev_q_out: the pool's dtype [rows][n_heads][head_dim], 16-byte aligned.
+ * A row whose position is outside the table is left out (TL_BAD_POSITION); a
+ * slot outside the pool is not written (TL_BAD_SLOT).  rows may be 0.
+ * n_heads a multiple of n_kv_heads. */
+int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t rows, int64_t row_stride, int32_t n_heads,
+                        const float* dev_q_gain, const float* dev_k_gain, float eps, const float* dev_table,
+                        int32_t length, const int32_t* dev_positions, const int64_t* dev_slots,
+                        const tl_kv_pool* pool, void* dev_q_out, int32_t* dev_status, void* cuda_stream);
+
+/* Attention of draft trees over a paged cache.  Request r has dev_ctx[r]
+ * positions in the cache and the nodes of rows cu[r] .. cu[r+1) - 1, whose keys
+ * and values are in the cache behind them (node j at position ctx + j, where
+ * tl_plan_batch and tl_norm_rope_append put it).  For node i and query head h
+ * (key head h / (n_heads / n_kv_heads)):
+ *   out = softmax_k(scale * q . key_k) value_k  over every position below ctx
+ *   and the nodes j whose bit j is set in the row's mask words.
+ * dev_masks NULL: node i sees nodes 0 .. i (a draft without branches, single
+ * tokens, or a block of prompt positions).  A row that sees nothing gives
+ * zeros and lse -infinity.  Keys and values that a row does not see never
+ * enter its result, NaN and infinities included; nor do positions on a page
+ * outside the pool (TL_BAD_PAGE).  Rows outside cu[0] .. cu[R] are left as
+ * they are.
+ *   dev_q: the pool's dtype, rows of [n_heads][head_dim], q_stride elements
+ *     apart; dev_out: out_dtype TL_F32 or the pool's, the same shape, out_stride
+ *     apart (both strides and addresses multiples of 16 bytes);
+ *   dev_lse: fp32 [rows][n_heads] natural-log sum of exponentials, or NULL;
+ *   n_rows: rows dev_q and dev_out hold;
+ *   max_nodes: the most nodes a request has; with masks <= 32 * mask_words.
+ *     A request with more nodes, with a negative length, with rows past n_rows
+ *     or with positions past max_pages is left out (TL_BAD_LENGTH);
+ *   scale: 0 means 1 / sqrt(head_dim);
+ *   dev_workspace: tl_tree_attention_workspace() bytes, 256-byte aligned; its
+ *     contents need no preparation and mean nothing afterwards, but calls that
+ *     may run at the same time need one each. */
+int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_kv_pool* pool, const int32_t* dev_block_table,
+                      int32_t max_pages, const int32_t* dev_ctx, const int32_t* dev_cu, int32_t R, int32_t n_rows,
+                      int32_t n_heads, int32_t max_nodes, const uint32_t* dev_masks, int32_t mask_words, float scale,
+                      void* dev_out, int32_t out_dtype, int64_t out_stride, float* dev_lse, void* dev_workspace,
+                      size_t workspace_bytes, int32_t* dev_status, void* cuda_stream);
+
+/* Workspace bytes of tl_tree_attention on the current device: depends on the
+ * head width and the rows per key head (max_nodes * n_heads / n_kv_heads)
+ * alone. */
+int tl_tree_attention_workspace(int32_t head_dim, int32_t n_heads, int32_t n_kv_heads, int32_t max_nodes,
+                                size_t* out_bytes);
+
 /* ---------------------------------------------------------- measurement -- */
 
 /* Read-bandwidth probe (a measurement aid, not a step of the model; the pages

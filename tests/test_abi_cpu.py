@@ -161,3 +161,103 @@ def test_workspace_holds_a_resident_fp16_copy_of_every_block():
     weights = T.weights_bytes(cfg)
     copies = (sh.n_pre + sh.n_loop_layers) * (4 * sh.d * sh.d + 3 * sh.d * sh.ffn) * 2
     assert ws > weights + copies
+
+
+# ------------------------------------------------------- serving operators --
+A = 0x1000  # an aligned address that nothing reads: every call here is refused before anything is enqueued
+
+
+def _pool(**kw):
+    f = dict(dev_pool=A, n_pages=4, dtype=_lib.TL_F16, n_kv_heads=2, head_dim=64, page_tokens=16)
+    f.update(kw)
+    return C.byref(_lib.TlKvPool(**f))
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=3), dict(dtype=-1), dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 20) + 1),
+                                dict(stride=9), dict(n_top=-1), dict(n_top=65), dict(n_top=11), dict(x=None),
+                                dict(x=A + 2), dict(targets=None), dict(n_top=0), dict(targets=A + 1), dict(ids=A + 2)])
+def test_token_logprobs_refusals(kw):
+    a = dict(x=A, dtype=_lib.TL_F32, rows=3, vocab=10, stride=10, targets=A, n_top=2, ids=A)
+    a.update(kw)
+    st = _lib.lib().tl_token_logprobs(a["x"], a["dtype"], a["rows"], a["vocab"], a["stride"], a["targets"], a["n_top"],
+                                      A, A, A, A, a["ids"], A, None)
+    assert st == _lib.TL_EINVAL
+
+
+def test_operators_with_nothing_to_do():
+    lib = _lib.lib()
+    assert lib.tl_token_logprobs(None, 0, 0, 10, 10, None, 0, None, None, None, None, None, None, None) == 0
+    assert lib.tl_norm_rope_append(None, 0, 0, 384, 2, None, None, 1e-6, None, 8, None, None, _pool(), None, None,
+                                   None) == 0
+    assert lib.tl_tree_attention(None, 128, _pool(), None, 4, None, None, 0, 0, 2, 1, None, 0, 0.0, None, 1, 128, None,
+                                 None, 0, None, None) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(R=0), dict(R=8193), dict(page=0), dict(page=24), dict(page=8192), dict(mp=0),
+                                dict(n_free=-1), dict(n_rows=-1), dict(words=9), dict(words=-1), dict(words=0),
+                                dict(masks=None), dict(cached=None), dict(head_out=A), dict(lens=A), dict(slots=A + 4),
+                                dict(free=None), dict(table=A + 2)])
+def test_plan_batch_refusals(kw):
+    a = dict(R=2, page=16, mp=4, n_free=3, n_rows=5, words=1, masks=A, cached=A, head_out=A + 64, lens=A + 128, slots=A,
+             free=A, table=A)
+    a.update(kw)
+    st = _lib.lib().tl_plan_batch(a["cached"], A, a["R"], a["page"], a["table"], a["mp"], a["free"], a["n_free"], A,
+                                  None, a["n_rows"], a["words"], A, a["lens"], A, a["head_out"], a["slots"], A,
+                                  a["masks"], None, None)
+    assert st == _lib.TL_EINVAL
+
+
+BAD_POOLS = [dict(dev_pool=None), dict(dev_pool=A + 8), dict(n_pages=0), dict(dtype=_lib.TL_F32), dict(n_kv_heads=0),
+             dict(head_dim=96), dict(page_tokens=8), dict(page_tokens=48), dict(page_tokens=2048),
+             dict(n_pages=1 << 26)]
+
+
+@pytest.mark.parametrize("kw", [dict(pool=p) for p in BAD_POOLS] + [
+    dict(dtype=4), dict(rows=-1), dict(stride=380), dict(stride=385), dict(heads=3), dict(heads=0), dict(gq=A),
+    dict(eps=-1.0), dict(eps=float("nan")), dict(length=0), dict(x=A + 8), dict(x=None), dict(slots=A + 4), dict(q=A + 2)])
+def test_norm_rope_append_refusals(kw):
+    a = dict(pool={}, dtype=_lib.TL_F16, rows=2, stride=384, heads=2, gq=None, eps=1e-6, length=8, x=A, slots=A, q=A)
+    a.update(kw)
+    st = _lib.lib().tl_norm_rope_append(a["x"], a["dtype"], a["rows"], a["stride"], a["heads"], a["gq"], None, a["eps"],
+                                        A, a["length"], A, a["slots"], _pool(**a["pool"]), a["q"], None, None)
+    assert st == _lib.TL_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(pool=p) for p in BAD_POOLS] + [
+    dict(qs=120), dict(qs=132), dict(heads=3), dict(heads=0), dict(R=-1), dict(rows=-1), dict(mp=0), dict(nodes=0),
+    dict(masks=None), dict(words=0), dict(nodes=33), dict(scale=-1.0), dict(scale=float("nan")),
+    dict(scale=float("inf")), dict(od=_lib.TL_BF16), dict(od=5), dict(os=120), dict(q=None), dict(q=A + 2),
+    dict(ws=None), dict(ws=A + 128), dict(lse=A + 1)])
+def test_tree_attention_refusals(kw):
+    a = dict(pool={}, qs=128, heads=2, R=2, rows=3, mp=4, nodes=8, masks=A, words=1, scale=0.0, od=_lib.TL_F16, os=128,
+             q=A, ws=A, lse=A)
+    a.update(kw)
+    st = _lib.lib().tl_tree_attention(a["q"], a["qs"], _pool(**a["pool"]), A, a["mp"], A, A, a["R"], a["rows"],
+                                      a["heads"], a["nodes"], a["masks"], a["words"], a["scale"], A, a["od"], a["os"],
+                                      a["lse"], a["ws"], 1 << 30, None, None)
+    assert st == _lib.TL_EINVAL
+
+
+def test_rope_table_refusals():
+    lib = _lib.lib()
+    for table, length, hd, base in ((None, 4, 64, 1e4), (A + 4, 4, 64, 1e4), (A, 0, 64, 1e4), (A, 4, 63, 1e4),
+                                    (A, 4, 0, 1e4), (A, 4, 64, 0.0), (A, 4, 64, float("nan"))):
+        assert lib.tl_rope_table(table, length, hd, base, None) == _lib.TL_EINVAL
+
+
+def test_operator_wrappers_refuse_host_tensors_and_shapes():
+    import torch
+    with pytest.raises(ValueError):
+        T.token_logprobs(torch.zeros(2, 3), None, n_top=1)
+    with pytest.raises(ValueError):
+        T.token_logprobs(torch.zeros(2, 3, 4))
+    with pytest.raises(ValueError):
+        T.token_logprobs(torch.zeros(2, 3, dtype=torch.float64))
+    z = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        T.plan_batch(z, z, torch.zeros(3, 4, dtype=torch.int32), z, z[:1], 16, 2)
+    pool = torch.zeros(2, 2, 1, 16, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        T.norm_rope_append(torch.zeros(2, 100), 1, pool, z.long(), z, torch.zeros(4, 32, 2))
+    with pytest.raises(ValueError):
+        T.tree_attention(torch.zeros(2, 1, 64), pool, torch.zeros(1, 4, dtype=torch.int32), z[:1], z, 1)
