@@ -6,12 +6,14 @@
 // One pass over the row.  A row is cut into chunks of 256 consecutive
 // elements; a warp takes a chunk at a time, 8 elements a lane, and keeps a
 // running maximum (uniform in the warp) with S and T rescaled when it rises.
-// The chunk maxima that this needs anyway are kept in shared memory: the n
-// first elements in the order (value descending, id ascending) lie in the n
-// chunks whose maxima come first in (maximum descending, chunk ascending),
-// since each chunk before an element's own holds an element before it.  So only
-// those n chunks are read again (they are in L2), filtered by the n-th chunk
-// maximum, and the few that pass are ordered.
+// The chunk maxima that this needs anyway are kept in shared memory.  A bound
+// on the n-th largest element comes from the threads' own maxima; only chunks
+// whose maxima reach it are read again (they are in L2), and the elements that
+// reach it, some tens, are ordered.  Where masks or equal logits let too many
+// through, the exact form: the n first elements in the order (value
+// descending, id ascending) lie in the n chunks whose maxima come first in
+// (maximum descending, chunk ascending), since each chunk before an element's
+// own holds an element before it.
 //
 // Few rows: a cluster of up to 8 CTAs shares a row and its first CTA merges the
 // partial sums and lists over distributed shared memory, with no scratch in
@@ -77,60 +79,235 @@ __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v)
 template <>
 __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Elements of one 16-byte word.
+// Two packed elements as floats, and the operations on packed words.
 template <class T>
-__device__ __forceinline__ void unpack(const uint4& w, float* f) {
-  const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) f[i] = to_f<T>(e[i]);
-}
+struct Word {};
+template <>
+struct Word<float> {
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  static constexpr float kPlain = 1e30f;  // below this, x - m is finite for finite x, and lowest - m an exponential of 0
+};
+template <>
+struct Word<__half> {
+  static constexpr uint32_t kNegInf = 0xfc00fc00u;
+  static constexpr float kPlain = 3e4f;
+  typedef __half2 V2;
+  static __device__ __forceinline__ V2 lowest() { return __halves2half2(__ushort_as_half(0xfbff), __ushort_as_half(0xfbff)); }
+  static __device__ __forceinline__ V2 both(float x) { return __float2half2_rn(x); }
+  static __device__ __forceinline__ float2 two(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static constexpr float kPlain = 1e30f;
+  typedef __nv_bfloat162 V2;
+  static __device__ __forceinline__ V2 lowest() {
+    return __halves2bfloat162(__ushort_as_bfloat16(0xff7f), __ushort_as_bfloat16(0xff7f));
+  }
+  static __device__ __forceinline__ V2 both(float x) { return __float2bfloat162_rn(x); }
+  static __device__ __forceinline__ float2 two(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r =
+        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
 
-// The lane's 8 elements of a chunk.  Positions are counted from the 16-byte
-// boundary at or before the row (`lead` elements before it), so whole words
-// are aligned; a word that holds the row's first or last elements is read by
-// element.  Elements outside the row are -inf.  Lane l holds, of each word w
-// of its 8 elements, positions base + w * 32 * E + l * E + (0 .. E-1).
+// A lane's 8 elements of a chunk, as they lie in memory.
 template <class T>
-__device__ __forceinline__ void load8(const T* row, int lead, int V, int64_t pos0, int lane, float* f) {
+struct Raw {
+  static constexpr int W = 8 * sizeof(T) / 16;
+  uint4 w[W];
+};
+
+// Positions are counted from the 16-byte boundary at or before the row (`lead`
+// elements before it), so whole words are aligned; a word that holds the row's
+// first or last elements is read by element.  Elements outside the row are
+// -inf.  Lane l holds, of each word w of its 8 elements, positions
+// base + w * 32 * E + l * E + (0 .. E-1).
+template <class T>
+__device__ __forceinline__ Raw<T> load_raw(const T* row, int lead, int V, int pos0, int lane) {
   constexpr int E = 16 / sizeof(T);  // elements of a word
+  Raw<T> r;
 #pragma unroll
-  for (int w = 0; w < 8 / E; ++w) {
-    const int64_t p = pos0 + (w * 32 + lane) * E - lead;  // element index of the word's first
+  for (int w = 0; w < Raw<T>::W; ++w) {
+    const int p = pos0 + (w * 32 + lane) * E - lead;  // element index of the word's first
     if (p >= 0 && p + E <= V) {
-      unpack<T>(__ldg(reinterpret_cast<const uint4*>(row + p)), f + w * E);
+      r.w[w] = __ldg(reinterpret_cast<const uint4*>(row + p));
     } else {
+      r.w[w] = make_uint4(Word<T>::kNegInf, Word<T>::kNegInf, Word<T>::kNegInf, Word<T>::kNegInf);
+      T* e = reinterpret_cast<T*>(&r.w[w]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[w * E + e] = (p + e >= 0 && p + e < V) ? to_f<T>(row[p + e]) : -INFINITY;
+      for (int i = 0; i < E; ++i)
+        if (p + i >= 0 && p + i < V) e[i] = row[p + i];
     }
+  }
+  return r;
+}
+// U chunks from chunk c on: one test for all of them, except at the row's ends.
+template <class T, int U>
+__device__ __forceinline__ void load_group(Raw<T> (&r)[U], const T* row, int lead, int V, int c, int lane) {
+  const int first = c * kChunk - lead;
+  if (first >= 0 && first + U * kChunk <= V) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + first) + lane;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int w = 0; w < Raw<T>::W; ++w) r[u].w[w] = __ldg(p + (u * Raw<T>::W + w) * 32);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = load_raw<T>(row, lead, V, (c + u) * kChunk, lane);
   }
 }
 template <class T>
-__device__ __forceinline__ int elem_index(int64_t pos0, int lead, int lane, int i) {
+__device__ __forceinline__ void unpack(const Raw<T>& r, float (&f)[8]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r.w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(u[i]);
+    } else {
+      const float2 v = Word<T>::two(u[i >> 1]);
+      f[i] = i & 1 ? v.y : v.x;
+    }
+  }
+}
+// -inf to the lowest number, whose exponential is 0 and 0 times which is not NaN.
+template <class T>
+__device__ __forceinline__ void raise_lowest(Raw<T>& r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r.w);
+#pragma unroll
+  for (int i = 0; i < 4 * Raw<T>::W; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      u[i] = __float_as_uint(fmaxf(__uint_as_float(u[i]), -3.4e38f));
+    } else {
+      const auto v = __hmax2(*reinterpret_cast<const typename Word<T>::V2*>(&u[i]), Word<T>::lowest());
+      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+}
+// How many of the lane's elements of U chunks are above x (EQ: at x or above).
+template <class T, int U, bool EQ>
+__device__ __forceinline__ int count_group(const Raw<T> (&r)[U], float x) {
+  if constexpr (sizeof(T) == 4) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(r[u].w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += EQ ? __uint_as_float(w[i]) >= x : __uint_as_float(w[i]) > x;
+    }
+    return n;
+  } else {
+    typedef typename Word<T>::V2 V2;
+    const V2 xx = Word<T>::both(x);
+    V2 s = Word<T>::both(0.f);  // counts up to 16, exact
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const V2* v = reinterpret_cast<const V2*>(r[u].w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = __hadd2(s, EQ ? __hge2(v[i], xx) : __hgt2(v[i], xx));
+    }
+    const float2 f = Word<T>::two(*reinterpret_cast<const uint32_t*>(&s));
+    return (int)(f.x + f.y);
+  }
+}
+// Largest of the 8, NaN if one is.
+template <class T>
+__device__ __forceinline__ float max8(const Raw<T>& r) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r.w);
+  if constexpr (sizeof(T) == 4) {
+    float m = __uint_as_float(u[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(u[i]));
+    return m;
+  } else {
+    const float2 v = Word<T>::two(Word<T>::max2(Word<T>::max2(u[0], u[1]), Word<T>::max2(u[2], u[3])));
+    return max_nan(v.x, v.y);
+  }
+}
+template <class T>
+__device__ __forceinline__ void load8(const T* row, int lead, int V, int pos0, int lane, float (&f)[8]) {
+  unpack<T>(load_raw<T>(row, lead, V, pos0, lane), f);
+}
+template <class T>
+__device__ __forceinline__ int elem_index(int pos0, int lead, int lane, int i) {
   constexpr int E = 16 / sizeof(T);
-  return (int)(pos0 + ((i / E) * 32 + lane) * E + i % E - lead);
+  return pos0 + ((i / E) * 32 + lane) * E + i % E - lead;
+}
+
+// Largest over the warp, NaN if one is.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Two fp32 values in one 64-bit register: the packed operations of sm_100.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_out(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
 struct Part {  // a CTA's share of a row
   double S, T;
   float m;
   int32_t before;
-  int32_t n_keys;
   int32_t nan;
 };
 
+// The lanes' (sum, weighted sum, maximum, count), joined; a NaN maximum marks a part that holds one.
+__device__ __forceinline__ Part merge_parts(double S, double T, float m, int before) {
+  Part p;
+  p.nan = __any_sync(0xffffffffu, m != m);
+  p.m = warp_max(m != m ? -INFINITY : m);
+  const double d = (double)p.m - (double)m, k = m > -INFINITY ? exp(-d) : 0.0;
+  p.S = warp_sum_d(k * S);
+  p.T = warp_sum_d(m > -INFINITY ? k * (T - d * S) : 0.0);
+  p.before = __reduce_add_sync(0xffffffffu, before);
+  return p;
+}
+
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  extern __shared__ uint32_t leaders[];  // [n_chunks] sort keys of the chunk maxima
-  __shared__ Part part;
+  extern __shared__ uint32_t leaders[];  // [n_chunks] chunk maxima; their sort keys from the search on
+  __shared__ Part part, merged;
   __shared__ double wS[kWarps], wT[kWarps];
   __shared__ float wm[kWarps];
   __shared__ int32_t wcnt[kWarps];
   __shared__ unsigned long long top[kMaxTop];               // this CTA's first n keys, in order
   __shared__ unsigned long long cand[kCand];
   __shared__ int32_t sel[kMaxTop];
-  __shared__ int32_t n_cand, n_sel, thr_chunk;
+  __shared__ uint32_t tmax[kThreads];
+  __shared__ int32_t n_cand, n_sel, n_keys;
   __shared__ uint32_t thr_key;
   __shared__ unsigned long long best_w[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -140,124 +317,243 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
   const T* row = reinterpret_cast<const T*>(a.x) + r * a.stride;
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
   const int all_chunks = (V + lead + kChunk - 1) / kChunk;
-  const int per = (all_chunks + cs - 1) / cs;
+  // whole groups of U chunks per CTA; those past the row's end read as -inf
+  constexpr int U = 4 / Raw<T>::W;
+  const int per = ((all_chunks + cs - 1) / cs + U - 1) / U * U;
   const int c0 = min(all_chunks, per * cr), c1 = min(all_chunks, c0 + per), nc = c1 - c0;
   const int t = a.targets ? a.targets[r] : -1;
   const bool has_t = t >= 0 && t < V;
   const float xt = has_t ? to_f<T>(row[t]) : 0.f;
 
   // ------------------------------------------------------------ one pass
-  float m = -INFINITY, S = 0.f, U = 0.f;
+  // U chunks of a warp at a time (64 bytes a lane), the next U on their way meanwhile.
+  float m = -INFINITY;
+  F2 S2 = f2(0.f, 0.f), T2 = f2(0.f, 0.f);
   int before = 0;
   bool nan = false;
-  for (int c = c0 + warp; c < c1; c += kWarps) {
-    float f[8];
-    const int64_t pos0 = (int64_t)c * kChunk;
-    load8<T>(row, lead, V, pos0, lane, f);
-    float mx = f[0];
+  float mine = -INFINITY;  // the thread's largest element
+  const F2 log2e = f2(kLog2e, kLog2e);
+  Raw<T> next[U];
+  load_group<T, U>(next, row, lead, V, c0 + warp * U, lane);
+  for (int cb = c0 + warp * U; cb < c1; cb += kWarps * U) {
+    Raw<T> cur[U];
+    float cm[U];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) mx = max_nan(mx, f[i]);
-    const uint32_t key = __reduce_max_sync(0xffffffffu, sort_key(mx));
-    if (lane == 0) leaders[c - c0] = key;
-    nan |= key == 0xffffffffu;
-    const float cm = key_value(key);
-    if (cm > m) {
-      const float d = cm - m, s = m == -INFINITY ? 0.f : ex2(-d * kLog2e);
-      U = m == -INFINITY ? 0.f : s * (U - d * S);
-      S *= s;
-      m = cm;
+    for (int u = 0; u < U; ++u) cur[u] = next[u];
+    if (cb + kWarps * U < c1) load_group<T, U>(next, row, lead, V, cb + kWarps * U, lane);
+    float top_m = -INFINITY;  // NaN if one is
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float lm = max8<T>(cur[u]);
+      mine = max_nan(mine, lm);
+      cm[u] = warp_max_nan(lm);
+      if (lane == 0) leaders[cb + u - c0] = __float_as_uint(cm[u]);
+      top_m = u == 0 ? cm[0] : max_nan(top_m, cm[u]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float z = fmaxf(f[i] - m, -1000.f);  // -inf (and -inf - -inf) to a value whose exponential is 0
-      const float e = ex2(z * kLog2e);
-      S += e;
-      U = fmaf(e, z, U);
+    if (!(top_m <= m)) {
+      nan |= top_m != top_m;
+      const float d = top_m - m, k = m == -INFINITY ? 0.f : ex2(-d * kLog2e);
+      const F2 kk = f2(k, k), dd = m == -INFINITY ? f2(0.f, 0.f) : f2(-d, -d);
+      T2 = mul2(kk, fma2(dd, S2, T2));
+      S2 = mul2(kk, S2);
+      m = fmaxf(m, top_m);  // past a NaN the sums mean nothing
     }
-    if (has_t) {
-      const int lo = (int)(pos0 - lead), hi = lo + kChunk;
-      if (hi <= t) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) before += f[i] >= xt && (lo >= 0 || elem_index<T>(pos0, lead, lane, i) >= 0);
-      } else if (lo > t) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) before += f[i] > xt;
+    if (has_t && top_m >= xt) {  // only chunks whose maximum reaches the target's logit hold tokens before it
+      const int lo = cb * kChunk - lead;
+      if (lo > t) {
+        before += count_group<T, U, false>(cur, xt);
+      } else if (lo >= 0 && lo + U * kChunk <= t) {
+        before += count_group<T, U, true>(cur, xt);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int id = elem_index<T>(pos0, lead, lane, i);
-          before += f[i] > xt || (f[i] == xt && id >= 0 && id < t);
+        for (int u = 0; u < U; ++u) {
+          float f[8];
+          unpack<T>(cur[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int id = elem_index<T>((cb + u) * kChunk, lead, lane, i);
+            before += f[i] > xt || (f[i] == xt && id >= 0 && id < t);
+          }
         }
+      }
+    }
+    if (fabsf(m) <= Word<T>::kPlain) {
+      const F2 mm = f2(-m, -m);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        raise_lowest<T>(cur[u]);
+        float f[8];
+        unpack<T>(cur[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const F2 z = add2(f2(f[i], f[i + 1]), mm);
+          float y0, y1;
+          f2_out(mul2(z, log2e), y0, y1);
+          const F2 e = f2(ex2(y0), ex2(y1));
+          S2 = add2(S2, e);
+          T2 = fma2(e, z, T2);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[8], s = 0.f, t1 = 0.f;
+        unpack<T>(cur[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float z = fmaxf(f[i] - m, -1000.f);  // also for -inf - -inf
+          const float e = ex2(z * kLog2e);
+          s += e;
+          t1 = fmaf(e, z, t1);
+        }
+        S2 = add2(S2, f2(s, 0.f));
+        T2 = add2(T2, f2(t1, 0.f));
       }
     }
   }
   {
-    const double s = warp_sum_d((double)S), u = warp_sum_d((double)U);
+    float s0, s1, t0, t1;
+    f2_out(S2, s0, s1);
+    f2_out(T2, t0, t1);
+    const double s = warp_sum_d((double)s0 + (double)s1), u = warp_sum_d((double)t0 + (double)t1);
     before = __reduce_add_sync(0xffffffffu, before);
     if (lane == 0) { wS[warp] = s; wT[warp] = u; wm[warp] = nan ? __uint_as_float(0x7fc00000u) : m; wcnt[warp] = before; }
   }
+  tmax[threadIdx.x] = sort_key(mine);
   if (threadIdx.x == 0) n_cand = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    Part p{0.0, 0.0, -INFINITY, 0, 0, 0};
-    for (int w = 0; w < kWarps; ++w) { p.nan |= wm[w] != wm[w]; p.m = fmaxf(p.m, wm[w]); p.before += wcnt[w]; }
-    for (int w = 0; w < kWarps; ++w) {
-      if (!(wm[w] > -INFINITY)) continue;
-      const double d = (double)p.m - (double)wm[w], s = exp(-d);
-      p.S += s * wS[w];
-      p.T += s * (wT[w] - d * wS[w]);
-    }
-    part = p;
+  if (warp == 1) {  // beside warp 0's search: lane w takes warp w's sums
+    const bool in = lane < kWarps;
+    const Part p = merge_parts(in ? wS[lane] : 0.0, in ? wT[lane] : 0.0, in ? wm[lane] : -INFINITY,
+                               in ? wcnt[lane] : 0);
+    if (lane == 0) part = p;
   }
 
   // ------------------------------------- the first n_top keys of this CTA's part
   if (n_top > 0) {
-    if (warp == 0) {
-      // the n_top first chunks, in order: lane l owns chunks l, l + 32, ...
-      int taken = 0;
-      const int want = min(n_top, nc);
-      uint32_t bk = 0;
-      int bc = 0x7fffffff;
-      auto rescan = [&]() {
-        bk = 0;
-        bc = 0x7fffffff;
-        for (int c = lane; c < nc; c += 32) {
-          const uint32_t k = leaders[c];
-          if (k > bk) { bk = k; bc = c; }  // key 0 marks a chunk taken (no value has it)
-        }
-      };
-      rescan();
-      for (; taken < want; ++taken) {
-        const uint32_t k = __reduce_max_sync(0xffffffffu, bk);
-        const int c = (int)__reduce_min_sync(0xffffffffu, bk == k ? (unsigned)bc : 0x7fffffffu);
-        if (lane == 0) { sel[taken] = c; thr_key = k; thr_chunk = c; }
-        if ((c & 31) == lane) { leaders[c] = 0; rescan(); }
+    // A bound from disjoint groups of elements: the n_top-th largest of 32 (or
+    // 64) group maxima has n_top elements at or above it.  Every warp finds it
+    // from the threads' maxima, then takes the elements at or above it from the
+    // chunks whose maxima reach it.
+    uint32_t g0 = 0, g1 = 0;
+#pragma unroll
+    for (int j = 0; j < kWarps; j += 2) {
+      g0 = max(g0, tmax[j * 32 + lane]);
+      g1 = max(g1, tmax[j * 32 + 32 + lane]);
+    }
+    uint32_t bound;
+    if (n_top <= 20) {
+      const uint32_t g = max(g0, g1);
+      int rank = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t o = __shfl_sync(0xffffffffu, g, j);
+        rank += o > g || (o == g && j < lane);
       }
-      if (lane == 0) {
-        n_sel = want;
-        if (want < n_top) { thr_key = 0; thr_chunk = 0x7fffffff; }
+      bound = __reduce_max_sync(0xffffffffu, rank == n_top - 1 ? g : 0u);
+    } else {
+      int r0 = 0, r1 = 0;
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t a0 = __shfl_sync(0xffffffffu, g0, j), a1 = __shfl_sync(0xffffffffu, g1, j);
+        r0 += (a0 > g0 || (a0 == g0 && j < lane)) + (a1 > g0);
+        r1 += (a0 >= g1) + (a1 > g1 || (a1 == g1 && j < lane));
+      }
+      bound = __reduce_max_sync(0xffffffffu, max(r0 == n_top - 1 ? g0 : 0u, r1 == n_top - 1 ? g1 : 0u));
+    }
+    // adds the elements of chunk c at or above key `tk` (among equals, the first `ties` of the chunk)
+    auto gather = [&](int c, uint32_t tk, int ties) {
+      float f[8];
+      const int pos0 = (c0 + c) * kChunk;
+      load8<T>(row, lead, V, pos0, lane, f);
+      constexpr int E = 16 / sizeof(T);
+      uint32_t eq = 0;
+      int rank = 0;  // equals of the chunk before the lane's, word by word
+      if (ties < kChunk) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int id = elem_index<T>(pos0, lead, lane, e);
+          eq |= (uint32_t)(id >= 0 && id < V && sort_key(f[e]) == tk) << e;
+        }
+      }
+      uint32_t in = 0;
+      int words = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (ties < kChunk && e % E == 0) {
+          const int n = __popc(eq >> e & ((1u << E) - 1u));
+          int x = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          rank = words + x - n;
+          words += __shfl_sync(0xffffffffu, x, 31);
+        }
+        const int id = elem_index<T>(pos0, lead, lane, e);
+        const uint32_t k = sort_key(f[e]);
+        bool take = id >= 0 && id < V && k >= tk;
+        if (ties < kChunk && k == tk) take = take && rank++ < ties;
+        in |= (uint32_t)take << e;
+      }
+      if (in) {  // few lanes
+        int at = atomicAdd(&n_cand, __popc(in));  // any order: the keys hold the ids
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (in >> e & 1u) {
+            const uint32_t id = (uint32_t)elem_index<T>(pos0, lead, lane, e);
+            if (at < kCand) cand[at] = (unsigned long long)sort_key(f[e]) << 32 | (0xffffffffu - id);
+            ++at;
+          }
+      }
+      __syncwarp();
+    };
+    for (int i = 0; i < nc; i += kThreads) {  // the warps take chunks in turn
+      const int c = i + lane * kWarps + warp;
+      unsigned reach = __ballot_sync(0xffffffffu, c < nc && sort_key(__uint_as_float(leaders[c])) >= bound);
+      while (reach) {
+        gather(i + (__ffs(reach) - 1) * kWarps + warp, bound, kChunk);
+        reach &= reach - 1;
       }
     }
     __syncthreads();
-    // elements at or before the last selected chunk's maximum
-    const uint32_t tk = thr_key;
-    const int tc = thr_chunk, ns = n_sel;
-    for (int i = warp; i < ns; i += kWarps) {
-      const int c = sel[i];
-      float f[8];
-      const int64_t pos0 = (int64_t)(c0 + c) * kChunk;
-      load8<T>(row, lead, V, pos0, lane, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int id = elem_index<T>(pos0, lead, lane, e);
-        const uint32_t k = sort_key(f[e]);
-        const bool in = id >= 0 && id < V && (k > tk || (k == tk && c <= tc));
-        const unsigned bal = __ballot_sync(0xffffffffu, in);
-        int at = 0;
-        if (lane == 0 && bal) at = atomicAdd(&n_cand, __popc(bal));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(bal & ((1u << lane) - 1u));
-        if (in && at < kCand) cand[at] = (unsigned long long)k << 32 | (0xffffffffu - (uint32_t)id);
+    int ns = 0;
+    if (n_cand > kCand) {
+      // Many at the bound (masked or constant rows) or few chunks holding all the best: the n_top first chunks
+      // exactly, in the order of their maxima; of elements equal to the last one's, n_top of a chunk at most.
+      __syncthreads();
+      if (threadIdx.x == 0) n_cand = 0;
+      if (warp == 0) {  // lane l owns chunks l, l + 32, ...
+        int taken = 0;
+        const int want = min(n_top, nc);
+        uint32_t bk = 0;
+        int bc = 0x7fffffff;
+        for (int c = lane; c < nc; c += 32) leaders[c] = sort_key(__uint_as_float(leaders[c]));
+        auto rescan = [&]() {
+          bk = 0;
+          bc = 0x7fffffff;
+          for (int c = lane; c < nc; c += 32) {
+            const uint32_t k = leaders[c];
+            if (k > bk) { bk = k; bc = c; }  // key 0 marks a chunk taken (no value has it)
+          }
+        };
+        rescan();
+        for (; taken < want; ++taken) {
+          const uint32_t k = __reduce_max_sync(0xffffffffu, bk);
+          const int c = (int)__reduce_min_sync(0xffffffffu, bk == k ? (unsigned)bc : 0x7fffffffu);
+          if (lane == 0) { sel[taken] = c; thr_key = k; }
+          if ((c & 31) == lane) { leaders[c] = 0; rescan(); }
+        }
+        if (lane == 0) {
+          n_sel = want;
+          if (want < n_top) thr_key = 0;
+        }
       }
+      __syncthreads();
+      ns = n_sel;
+      const uint32_t tk = thr_key;
+      for (int i = warp; i < ns; i += kWarps) gather(sel[i], tk, n_top);
     }
     __syncthreads();
     const int n = n_cand, out = min(n_top, n);
@@ -295,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
         unsigned long long best = 0;
         for (int i = warp; i < ns; i += kWarps) {
           float f[8];
-          const int64_t pos0 = (int64_t)(c0 + sel[i]) * kChunk;
+          const int pos0 = (c0 + sel[i]) * kChunk;
           load8<T>(row, lead, V, pos0, lane, f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -319,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
       }
     }
     __syncthreads();
-    if (threadIdx.x == 0) part.n_keys = out;
+    if (threadIdx.x == 0) n_keys = out;
   }
 
   // ------------------------------------------------- merge over the cluster
@@ -330,8 +626,7 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
       if (n_top > 0) {
         for (int i = threadIdx.x; i < cs * n_top; i += kThreads) {
           const int b = i / n_top, j = i % n_top;
-          const Part* pb = cluster.map_shared_rank(&part, b);
-          cand[i] = j < pb->n_keys ? cluster.map_shared_rank(top, b)[j] : 0ull;
+          cand[i] = j < *cluster.map_shared_rank(&n_keys, b) ? cluster.map_shared_rank(top, b)[j] : 0ull;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < cs * n_top; i += kThreads) {
@@ -349,22 +644,11 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
           if (rank < n_top) top[rank] = k;
         }
       }
-      if (threadIdx.x == 0) {
-        Part p{0.0, 0.0, -INFINITY, 0, 0, 0};
-        for (int b = 0; b < cs; ++b) {
-          const Part q = *cluster.map_shared_rank(&part, b);
-          p.nan |= q.nan;
-          p.m = fmaxf(p.m, q.m);
-          p.before += q.before;
-        }
-        for (int b = 0; b < cs; ++b) {
-          const Part q = *cluster.map_shared_rank(&part, b);
-          if (!(q.m > -INFINITY)) continue;
-          const double d = (double)p.m - (double)q.m, s = exp(-d);
-          p.S += s * q.S;
-          p.T += s * (q.T - d * q.S);
-        }
-        part = p;
+      if (warp == 1) {
+        Part q{0.0, 0.0, -INFINITY, 0, 0};
+        if (lane < cs) q = *cluster.map_shared_rank(&part, lane);
+        const Part p = merge_parts(q.S, q.T, q.nan ? __uint_as_float(0x7fc00000u) : q.m, q.before);
+        if (lane == 0) merged = p;
       }
     }
     cluster.sync();
@@ -374,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 4) kernel(Args a) {
   if (cr != 0) return;
 
   // ------------------------------------------------------------- outputs
-  const Part p = part;
+  const Part p = cs > 1 ? merged : part;
   const bool bad = p.nan || p.m == INFINITY, none = p.m == -INFINITY;
   const float qnan = __uint_as_float(0x7fc00000u);
   const double lnS = none || bad ? 0.0 : log(p.S);
@@ -401,7 +685,7 @@ static int launch(Args a, cudaStream_t s) {
   int cs = 1;
   while (cs < kMaxCluster && a.rows * cs < 4 * sms && a.V >= 2 * cs * kWarps * kChunk) cs *= 2;
   const int chunks = (a.V + 8 + kChunk - 1) / kChunk;
-  a.n_chunks = (chunks + cs - 1) / cs;
+  a.n_chunks = (chunks + cs - 1) / cs + 4;  // rounded up to groups of 4 at most
   const int64_t most = 0x7fffffff / kMaxCluster;  // rows of one launch
   for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
     Args b = a;
@@ -426,7 +710,7 @@ static int launch(Args a, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    TL_CUDA(cudaLaunchKernelEx(&lc, kernel<T>, b));
+    TL_CUDA(cudaLaunchKernelEx(&lc, logprobs_kernel<T>, b));
   }
   return check_cuda(cudaGetLastError());
 }

@@ -80,7 +80,7 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
 }
 
 template <class TI, class TC, int HD>
-__global__ void __launch_bounds__(kThreads) kernel(Args a) {
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   constexpr int LT = HD / 16;  // lanes of a head
   const int heads = a.H + 2 * a.Hk;
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LT;
@@ -160,9 +160,9 @@ static int launch(const Args& a, int hd, cudaStream_t s) {
   const int64_t grid = (threads + kThreads - 1) / kThreads;
   if (grid > 0x7fffffff) return TL_EINVAL;
   switch (hd) {
-    case 32: kernel<TI, TC, 32><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
-    case 64: kernel<TI, TC, 64><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
-    default: kernel<TI, TC, 128><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
+    case 32: norm_rope_kernel<TI, TC, 32><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
+    case 64: norm_rope_kernel<TI, TC, 64><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
+    default: norm_rope_kernel<TI, TC, 128><<<(unsigned)grid, kThreads, 0, s>>>(a); break;
   }
   return check_cuda(cudaGetLastError());
 }

@@ -58,7 +58,7 @@ __device__ __forceinline__ Req request(const Args& a, int r) {
   return q;
 }
 
-__global__ void __launch_bounds__(kThreads) kernel(Args a) {
+__global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
   extern __shared__ int32_t sh[];
   int32_t* cu = sh;                // [R + 1]
   int32_t* off = sh + a.R + 1;     // [R] pages taken before the request; -1: refused
@@ -212,10 +212,10 @@ extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh
   while ((1 << a.shift) < page_tokens) ++a.shift;
   const size_t smem = (size_t)(2 * R + 1) * 4;  // at most 64 KB
   if (smem > 46 * 1024)
-    TL_CUDA(cudaFuncSetAttribute(plan::kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    TL_CUDA(cudaFuncSetAttribute(plan::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   const int64_t by_rows = ((int64_t)n_rows + plan::kThreads - 1) / plan::kThreads;
   const int64_t by_req = ((int64_t)R + plan::kThreads / 32 - 1) / (plan::kThreads / 32);
   const int64_t grid = by_rows > by_req ? by_rows : by_req;
-  plan::kernel<<<(unsigned)(grid < 592 ? grid : 592), plan::kThreads, smem, (cudaStream_t)cuda_stream>>>(a);
+  plan::plan_kernel<<<(unsigned)(grid < 592 ? grid : 592), plan::kThreads, smem, (cudaStream_t)cuda_stream>>>(a);
   return check_cuda(cudaGetLastError());
 }

@@ -208,7 +208,7 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_to
 
 template <int HD, int WM, bool BF>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
+tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
   using C = Cfg<HD>;
   constexpr int KT = C::KT, BM = 16 * WM, WN = 4 / WM, KW = KT / WN, NT = KW / 8;
   extern __shared__ __align__(1024) uint8_t smem_ta[];
@@ -564,7 +564,7 @@ attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
 // the cut at the start of range b, and acts if it is the first of its block.
 // blockIdx.y: 4 rows of the block.
 template <int HD, int BM, bool BF>
-__global__ void __launch_bounds__(128) join_kernel(const TreeAttnArgs a) {
+__global__ void __launch_bounds__(128) tree_join_kernel(const TreeAttnArgs a) {
   constexpr int KT = Cfg<HD>::KT;
   pdl_wait();
   const int G = gridDim.x, b = blockIdx.x;
@@ -615,7 +615,7 @@ static int block_rows(int64_t rows_per_head) { return rows_per_head <= 16 ? 16 :
 
 template <int HD, int WM, bool BF>
 static int launch(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cudaStream_t s) {
-  auto kern = attn_kernel<HD, WM, BF>;
+  auto kern = tree_attn_kernel<HD, WM, BF>;
   TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM));
   kern<<<n_sms, kThreads, Cfg<HD>::SMEM, s>>>(map, a);
   TL_CUDA(cudaGetLastError());
@@ -628,7 +628,7 @@ static int launch(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cuda
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  TL_CUDA(cudaLaunchKernelEx(&lc, join_kernel<HD, 16 * WM, BF>, a));
+  TL_CUDA(cudaLaunchKernelEx(&lc, tree_join_kernel<HD, 16 * WM, BF>, a));
   return check_cuda(cudaGetLastError());
 }
 
