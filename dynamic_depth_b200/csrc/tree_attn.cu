@@ -50,11 +50,15 @@ struct Cfg {
   static constexpr int ROWB = COLS * 2;             // bytes of a box row
   static constexpr int TILE = KT * ROWB;
   static constexpr int STAGE = 2 * CT * TILE;       // K boxes, then V boxes
-  static constexpr int STAGES = HD == 32 ? 8 : 5;
+  // Even, so that a stage always belongs to the same group of warps: with an odd number, a group ahead of the
+  // other could wait for a stage's next round while this round's copy is still in flight, and a wait by parity
+  // takes the round before for it.
+  static constexpr int STAGES = HD == 32 ? 8 : 4;
   static constexpr int SLOT = (HD / 2 + 4) * 32;    // floats of one warp's state: output, 2 maxima, 2 sums
   static constexpr int MERGE = 4 * SLOT * 4;
   static constexpr int SMEM = 1024 + STAGES * STAGE + MERGE + 256;
   static_assert(SMEM <= 227 * 1024, "tile ring does not fit");
+  static_assert(STAGES % 2 == 0, "a stage serves one group of warps");
 };
 
 // Start of each CTA's range, for the joining kernel.
