@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace tl {
@@ -68,12 +69,6 @@ struct Start {
   int32_t r;
   int32_t pad;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -178,7 +173,7 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_to
   long long total = 0, u0 = 0, pre = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long run = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+    for (int r0 = 0; r0 < a.R; r0 += blockDim.x) {
       const int r = r0 + threadIdx.x;
       long long x = 0;
       if (r < a.R) {
@@ -196,7 +191,7 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_to
       if (lane == 31) wsum[warp] = x;
       __syncthreads();
       pre = run + x - mine;
-      for (int w = 0; w < kWarps + 1; ++w) {
+      for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w < warp) pre += wsum[w];
         run += wsum[w];
       }
@@ -209,6 +204,68 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_to
   }
   if (threadIdx.x == 0) *sh_total = total;
 }
+
+// The producer warp: the tiles of the CTA's range into the ring, a box per page
+// (or part of one), K and V of each.
+template <class C, int KT, int BM>
+__device__ __forceinline__ void produce(const TreeAttnArgs& a, const CUtensorMap& kvmap, Walk<KT, BM> walk,
+                                        uint8_t* ring, uint64_t* full, uint64_t* empty, volatile uint32_t* info,
+                                        volatile int32_t* abort_flag) {
+  constexpr int ROWB = C::TILE / KT;
+  const int lane = threadIdx.x & 31;
+  const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR;
+  Seg s;
+  int k = 0;
+  bool ok = true;
+  while (ok && walk.next(a, s)) {
+    const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
+    auto page_of = [&](int t) {
+      const int pos = t * KT + lane * PR;
+      return lane < boxes && pos < s.q.len ? __ldg(table + (pos >> a.page_shift)) : -1;
+    };
+    int page = page_of(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++k) {
+      const int next_page = t + 1 < s.t1 ? page_of(t + 1) : -1;
+      const int st = k % C::STAGES, round = k / C::STAGES;
+      if (round > 0 && !mbar_wait_warp(smem_u32(&empty[st]), (round - 1) & 1, abort_flag)) { ok = false; break; }
+      const int pos = t * KT + lane * PR;
+      const bool want = lane < boxes && pos < s.q.len;
+      const bool good = want && page >= 0 && page < a.n_pages;
+      if (want && !good && a.status) atomicOr(a.status, TL_BAD_PAGE);
+      const uint32_t in = __ballot_sync(0xffffffffu, good);
+      const uint32_t bar = smem_u32(&full[st]);
+      if (lane == 0) {
+        info[st] = in;
+        mbar_expect_tx(bar, __popc(in) * 2 * C::CT * PR * ROWB);
+      }
+      __syncwarp();
+      if (good) {
+        const int64_t y = (((int64_t)page * 2 * a.Hk + s.hk) << a.page_shift) + (pos & (P - 1));
+        const uint32_t dst = smem_u32(ring + st * C::STAGE) + lane * PR * ROWB;
+#pragma unroll
+        for (int ct = 0; ct < C::CT; ++ct) {
+          tma_load_2d(dst + ct * C::TILE, &kvmap, ct * 64, (int)y, bar);
+          tma_load_2d(dst + (C::CT + ct) * C::TILE, &kvmap, ct * 64, (int)(y + ((int64_t)a.Hk << a.page_shift)), bar);
+        }
+      }
+      __syncwarp();
+      page = next_page;
+    }
+  }
+  if (!ok && lane == 0) {  // let the copies in flight land
+    volatile int32_t never = 0;
+    for (int i = k > C::STAGES ? k - C::STAGES : 0; i < k; ++i)
+      mbar_wait(smem_u32(&full[i % C::STAGES]), (i / C::STAGES) & 1, &never);
+  }
+}
+
+}  // namespace tree
+}  // namespace tl
+
+#include "tree_attn_tc.cuh"
+
+namespace tl {
+namespace tree {
 
 template <int HD, int WM, bool BF>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -260,49 +317,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
     Seg s;
     int k = 0;  // tiles of this CTA so far
     if (warp == kWarps) {
-      // ------------------------------------------------------------ producer
-      bool ok = true;
-      while (ok && walk.next(a, s)) {
-        const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
-        auto page_of = [&](int t) {
-          const int pos = t * KT + lane * PR;
-          return lane < boxes && pos < s.q.len ? __ldg(table + (pos >> a.page_shift)) : -1;
-        };
-        int page = page_of(s.t0);
-        for (int t = s.t0; t < s.t1; ++t, ++k) {
-          const int next_page = t + 1 < s.t1 ? page_of(t + 1) : -1;
-          const int st = k % C::STAGES, round = k / C::STAGES;
-          if (round > 0 && !mbar_wait_warp(smem_u32(&empty[st]), (round - 1) & 1, abort_flag)) { ok = false; break; }
-          const int pos = t * KT + lane * PR;
-          const bool want = lane < boxes && pos < s.q.len;
-          const bool good = want && page >= 0 && page < a.n_pages;
-          if (want && !good && a.status) atomicOr(a.status, TL_BAD_PAGE);
-          const uint32_t in = __ballot_sync(0xffffffffu, good);
-          const uint32_t bar = smem_u32(&full[st]);
-          if (lane == 0) {
-            info[st] = in;
-            mbar_expect_tx(bar, __popc(in) * 2 * C::CT * PR * C::ROWB);
-          }
-          __syncwarp();
-          if (good) {
-            const int64_t y = (((int64_t)page * 2 * a.Hk + s.hk) << a.page_shift) + (pos & (P - 1));
-            const uint32_t dst = smem_u32(ring + st * C::STAGE) + lane * PR * C::ROWB;
-#pragma unroll
-            for (int ct = 0; ct < C::CT; ++ct) {
-              tma_load_2d(dst + ct * C::TILE, &kvmap, ct * 64, (int)y, bar);
-              tma_load_2d(dst + (C::CT + ct) * C::TILE, &kvmap, ct * 64, (int)(y + ((int64_t)a.Hk << a.page_shift)),
-                          bar);
-            }
-          }
-          __syncwarp();
-          page = next_page;
-        }
-      }
-      if (!ok && lane == 0) {  // let the copies in flight land
-        volatile int32_t never = 0;
-        for (int i = k > C::STAGES ? k - C::STAGES : 0; i < k; ++i)
-          mbar_wait(smem_u32(&full[i % C::STAGES]), (i / C::STAGES) & 1, &never);
-      }
+      produce<C, KT, BM>(a, kvmap, walk, ring, full, empty, info, abort_flag);
     } else {
       // ----------------------------------------------------------- consumers
       const int grp = warp >> 2, wm = (warp & 3) % WM, wn = (warp & 3) / WM;
@@ -566,10 +581,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 
 // Joins the pieces of the row blocks that the CTAs' ranges cut: CTA b looks at
 // the cut at the start of range b, and acts if it is the first of its block.
-// blockIdx.y: 4 rows of the block.
-template <int HD, int BM, bool BF>
+// A warp a row, the rows of the block dealt over blockIdx.y.
+template <int HD, int KT, int BM, bool BF>
 __global__ void __launch_bounds__(128) tree_join_kernel(const TreeAttnArgs a) {
-  constexpr int KT = Cfg<HD>::KT;
   pdl_wait();
   const int G = gridDim.x, b = blockIdx.x;
   const Start st = reinterpret_cast<const Start*>(a.ws)[b];
@@ -582,49 +596,61 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeAttnArgs a) {
   const int64_t item = (u - st.base) / q.tiles, ua = st.base + item * q.tiles, ub = ua + q.tiles;
   if (u == ua || owner(ua) != owner(u - 1)) return;
   const int hk = (int)(item / q.blocks), blk = (int)(item - (int64_t)hk * q.blocks), grp = a.H / a.Hk;
-  const int rr = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int y = blockIdx.y * 4 + rr, rho = blk * BM + y;
-  if (rho >= q.n * grp) return;
+  const int lane = threadIdx.x & 31, rows = min(BM, q.n * grp - blk * BM);
   const float* ws = reinterpret_cast<const float*>(a.ws + G * sizeof(Start));
-  float m = -INFINITY, l = 0.f, O[HD / 32];
+  for (int y = blockIdx.y * 4 + (threadIdx.x >> 5); y < rows; y += gridDim.y * 4) {
+    float m = -INFINITY, l = 0.f, O[HD / 32];
 #pragma unroll
-  for (int e = 0; e < HD / 32; ++e) O[e] = 0.f;
-  for (int c = owner(ua); c < G;) {
-    const float* w = ws + ((int64_t)c * 2 + (ua < first(c) ? 0 : 1)) * BM * (HD + 2) + y * (HD + 2);
-    const float m2 = w[0], l2 = w[1], mn = fmaxf(m, m2), z = mn == -INFINITY ? 0.f : mn;
-    const float x = ex2(m - z), x2 = ex2(m2 - z);
-    l = l * x + l2 * x2;
+    for (int e = 0; e < HD / 32; ++e) O[e] = 0.f;
+    for (int c = owner(ua); c < G;) {
+      const float* w = ws + ((int64_t)c * 2 + (ua < first(c) ? 0 : 1)) * BM * (HD + 2) + y * (HD + 2);
+      const float m2 = w[0], l2 = w[1], mn = fmaxf(m, m2), z = mn == -INFINITY ? 0.f : mn;
+      const float x = ex2(m - z), x2 = ex2(m2 - z);
+      l = l * x + l2 * x2;
 #pragma unroll
-    for (int e = 0; e < HD / 32; ++e) O[e] = O[e] * x + w[2 + e * 32 + lane] * x2;
-    m = mn;
-    if (first(c + 1) >= ub) break;
-    c = owner(first(c + 1));
+      for (int e = 0; e < HD / 32; ++e) O[e] = O[e] * x + w[2 + e * 32 + lane] * x2;
+      m = mn;
+      if (first(c + 1) >= ub) break;
+      c = owner(first(c + 1));
+    }
+    const int rho = blk * BM + y, node = rho / grp, head = hk * grp + rho - node * grp;
+    const int64_t row = q.row0 + node;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e) {
+      const float v = O[e] * inv;
+      const int64_t o = row * a.out_stride + (int64_t)head * HD + e * 32 + lane;
+      if (a.out_f32) static_cast<float*>(a.out)[o] = v;
+      else if constexpr (BF) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+      else static_cast<__half*>(a.out)[o] = __float2half_rn(v);
+      if (a.out16) act16_put(a.out16, row, a.H * HD, head * HD + e * 32 + lane, v, a.split16);
+    }
+    if (a.lse && lane == 0) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
-  const int node = rho / grp, head = hk * grp + rho - node * grp;
-  const int64_t row = q.row0 + node;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < HD / 32; ++e) {
-    const float v = O[e] * inv;
-    const int64_t o = row * a.out_stride + (int64_t)head * HD + e * 32 + lane;
-    if (a.out_f32) static_cast<float*>(a.out)[o] = v;
-    else if constexpr (BF) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(a.out)[o] = __float2half_rn(v);
-    if (a.out16) act16_put(a.out16, row, a.H * HD, head * HD + e * 32 + lane, v, a.split16);
-  }
-  if (a.lse && lane == 0) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-static int block_rows(int64_t rows_per_head) { return rows_per_head <= 16 ? 16 : rows_per_head <= 32 ? 32 : 64; }
+// Rows of a block: the smallest that holds a request's rows of a key head.  More than 32 rows of widths 64 and 128
+// take the tensor-core kernel's 128.
+static int block_rows(int hd, int64_t rows_per_head) {
+  if (rows_per_head <= 16) return 16;
+  if (rows_per_head <= 32) return 32;
+  return hd >= 64 ? 128 : 64;
+}
 
-template <int HD, int WM, bool BF>
-static int launch(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cudaStream_t s) {
-  auto kern = tree_attn_kernel<HD, WM, BF>;
-  TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM));
-  kern<<<n_sms, kThreads, Cfg<HD>::SMEM, s>>>(map, a);
+template <int HD, int KT, int BM, bool BF, class K>
+static int launch(K kern, int threads, int smem, const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms,
+                  cudaStream_t s) {
+  constexpr int cols = HD < 64 ? HD : 64;
+  CUtensorMap map;
+  const uint64_t rows = (uint64_t)p.n_pages * 2 * p.n_kv_heads * p.page_tokens;
+  TL_TRY(encode_map_2d(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.dev_pool, HD,
+                       rows, HD * 2, cols, p.page_tokens < KT ? p.page_tokens : KT,
+                       cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+  TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  kern<<<n_sms, threads, smem, s>>>(map, a);
   TL_CUDA(cudaGetLastError());
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(n_sms, 16 * WM / 4);
+  lc.gridDim = dim3(n_sms, BM / 16);
   lc.blockDim = dim3(128);
   lc.stream = s;
   cudaLaunchAttribute at[1];
@@ -632,29 +658,22 @@ static int launch(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cuda
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  TL_CUDA(cudaLaunchKernelEx(&lc, tree_join_kernel<HD, 16 * WM, BF>, a));
+  TL_CUDA(cudaLaunchKernelEx(&lc, tree_join_kernel<HD, KT, BM, BF>, a));
   return check_cuda(cudaGetLastError());
 }
 
 template <int HD, bool BF>
-static int launch_rows(const TreeAttnArgs& a, const CUtensorMap& map, int n_sms, cudaStream_t s) {
-  switch (block_rows((int64_t)a.max_nodes * (a.H / a.Hk))) {
-    case 16: return launch<HD, 1, BF>(a, map, n_sms, s);
-    case 32: return launch<HD, 2, BF>(a, map, n_sms, s);
-    default: return launch<HD, 4, BF>(a, map, n_sms, s);
-  }
-}
-
-template <int HD>
 static int run(const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms, cudaStream_t s) {
   using C = Cfg<HD>;
-  CUtensorMap map;
-  const bool bf = p.dtype == TL_BF16;
-  const uint64_t rows = (uint64_t)p.n_pages * 2 * p.n_kv_heads * p.page_tokens;
-  TL_TRY(encode_map_2d(&map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.dev_pool, HD,
-                       rows, HD * 2, C::COLS, p.page_tokens < C::KT ? p.page_tokens : C::KT,
-                       C::ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
-  return bf ? launch_rows<HD, true>(a, map, n_sms, s) : launch_rows<HD, false>(a, map, n_sms, s);
+  switch (block_rows(HD, (int64_t)a.max_nodes * (a.H / a.Hk))) {
+    case 16: return launch<HD, C::KT, 16, BF>(tree_attn_kernel<HD, 1, BF>, kThreads, C::SMEM, a, p, n_sms, s);
+    case 32: return launch<HD, C::KT, 32, BF>(tree_attn_kernel<HD, 2, BF>, kThreads, C::SMEM, a, p, n_sms, s);
+    default:
+      if constexpr (HD == 32)
+        return launch<HD, C::KT, 64, BF>(tree_attn_kernel<HD, 4, BF>, kThreads, C::SMEM, a, p, n_sms, s);
+      else
+        return launch<HD, 128, 128, BF>(tree_attn_tc_kernel<HD, BF>, 256, TcCfg<HD>::SMEM, a, p, n_sms, s);
+  }
 }
 
 static int sm_count(int* n) {
@@ -667,7 +686,7 @@ static int sm_count(int* n) {
 }  // namespace tree
 
 size_t tree_attn_workspace(int hd, int64_t rows_per_head, int n_sms) {
-  return (size_t)n_sms * sizeof(tree::Start) + (size_t)n_sms * 2 * tree::block_rows(rows_per_head) * (hd + 2) * 4;
+  return (size_t)n_sms * sizeof(tree::Start) + (size_t)n_sms * 2 * tree::block_rows(hd, rows_per_head) * (hd + 2) * 4;
 }
 
 int tree_attn_run(TreeAttnArgs a, const tl_kv_pool& p, cudaStream_t s, int64_t* launches) {
@@ -678,10 +697,11 @@ int tree_attn_run(TreeAttnArgs a, const tl_kv_pool& p, cudaStream_t s, int64_t* 
   a.page_shift = 0;
   while ((1 << a.page_shift) < p.page_tokens) ++a.page_shift;
   if (launches) *launches += 2;
+  const bool bf = p.dtype == TL_BF16;
   switch (p.head_dim) {
-    case 32: return tree::run<32>(a, p, n_sms, s);
-    case 64: return tree::run<64>(a, p, n_sms, s);
-    default: return tree::run<128>(a, p, n_sms, s);
+    case 32: return bf ? tree::run<32, true>(a, p, n_sms, s) : tree::run<32, false>(a, p, n_sms, s);
+    case 64: return bf ? tree::run<64, true>(a, p, n_sms, s) : tree::run<64, false>(a, p, n_sms, s);
+    default: return bf ? tree::run<128, true>(a, p, n_sms, s) : tree::run<128, false>(a, p, n_sms, s);
   }
 }
 
