@@ -62,13 +62,35 @@ struct Cfg {
   static_assert(STAGES % 2 == 0, "a stage serves one group of warps");
 };
 
-// Start of each CTA's range, for the joining kernel.
-struct Start {
-  int64_t base;  // first unit of the request that holds the CTA's first unit
-  int64_t total; // units in all
-  int32_t r;
-  int32_t pad;
+struct Req {
+  int32_t row0, n, ctx, len, tiles, blocks;  // blocks: row blocks of a key head
+  bool bad;
 };
+
+// A CTA's range of units, and where its first unit lies; kept in the workspace
+// for the joining kernel.
+struct Range {
+  int64_t u0, u1;   // units of this CTA
+  int64_t base;     // first unit of the request that holds u0
+  int64_t ua, ub;   // units of the row block that holds u0
+  int32_t r, hk, blk, pad;
+  Req q;
+};
+
+// A piece of a row block in the workspace: (maximum, sum) of each row, then the
+// output as [hd / 4][BM] groups of four values, so that neighbouring rows are
+// neighbours in memory.  Two per CTA: 0 for a block that began in an earlier
+// range, 1 for one that goes on in the next.
+template <int HD, int BM>
+struct Piece {
+  float2 ml[BM];
+  float4 o[HD / 4][BM];
+};
+template <int HD, int BM>
+__device__ __forceinline__ Piece<HD, BM>* piece_of(const TreeAttnArgs& a, int ctas, int cta, int slot) {
+  const size_t head = ((size_t)ctas * sizeof(Range) + 255) / 256 * 256;
+  return reinterpret_cast<Piece<HD, BM>*>(a.ws + head) + (size_t)cta * 2 + slot;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -112,11 +134,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-
-struct Req {
-  int32_t row0, n, ctx, len, tiles, blocks;  // blocks: row blocks of a key head
-  bool bad;
-};
 
 template <int KT, int BM>
 __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r) {
@@ -165,19 +182,20 @@ struct Walk {
   }
 };
 
-// Block-wide: total units, and the request that holds this CTA's first unit.
+// Block-wide: this CTA's range (valid after a __syncthreads).  Up to blockDim.x
+// requests are read once; more take a second pass over the lengths.
 template <int KT, int BM>
-__device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_total, Start* sh_start,
-                                           long long* wsum) {
+__device__ __forceinline__ void find_range(const TreeAttnArgs& a, Range* sh, long long* wsum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long total = 0, u0 = 0, pre = 0;
+  long long total = 0, u0 = 0, u1 = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long run = 0;
     for (int r0 = 0; r0 < a.R; r0 += blockDim.x) {
       const int r = r0 + threadIdx.x;
       long long x = 0;
+      Req q;
       if (r < a.R) {
-        const Req q = request<KT, BM>(a, r);
+        q = request<KT, BM>(a, r);
         x = (long long)q.tiles * q.blocks * a.Hk;
         if (pass == 0 && q.bad && blockIdx.x == 0 && a.status) atomicOr(a.status, TL_BAD_LENGTH);
       }
@@ -190,19 +208,33 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, int64_t* sh_to
       __syncthreads();
       if (lane == 31) wsum[warp] = x;
       __syncthreads();
-      pre = run + x - mine;
+      long long pre = run + x - mine;
       for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w < warp) pre += wsum[w];
         run += wsum[w];
       }
-      if (pass == 1 && mine > 0 && u0 >= pre && u0 < pre + mine) *sh_start = Start{pre, total, r, 0};
+      if (a.R <= (int)blockDim.x) {
+        u0 = run * blockIdx.x / gridDim.x;
+        u1 = run * (blockIdx.x + 1) / gridDim.x;
+      }
+      if ((pass == 1 || a.R <= (int)blockDim.x) && u0 < u1 && mine > 0 && u0 >= pre && u0 < pre + mine) {
+        const int64_t item = (u0 - pre) / q.tiles;
+        const int hk = (int)(item / q.blocks);
+        *sh = Range{u0, u1, pre, pre + item * q.tiles, pre + (item + 1) * q.tiles, r, hk,
+                    (int)(item - (int64_t)hk * q.blocks), 0, q};
+        reinterpret_cast<Range*>(a.ws)[blockIdx.x] = *sh;
+      }
     }
-    if (pass == 0) {
-      total = run;
-      u0 = total * blockIdx.x / gridDim.x;
-    }
+    if (a.R <= (int)blockDim.x) break;
+    total = run;
+    u0 = total * blockIdx.x / gridDim.x;
+    u1 = total * (blockIdx.x + 1) / gridDim.x;
   }
-  if (threadIdx.x == 0) *sh_total = total;
+  if (threadIdx.x == 0 && u0 >= u1) {  // nothing to do
+    sh->u0 = sh->u1 = u0;
+    reinterpret_cast<Range*>(a.ws)[blockIdx.x].u0 = u0;
+    reinterpret_cast<Range*>(a.ws)[blockIdx.x].u1 = u0;
+  }
 }
 
 // The producer warp: the tiles of the CTA's range into the ring, a box per page
@@ -279,8 +311,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
   uint64_t* empty = full + C::STAGES;
   volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(empty + C::STAGES);  // [STAGES] boxes that landed
   __shared__ int32_t abort_s;
-  __shared__ int64_t total_s;
-  __shared__ Start start_s;
+  __shared__ Range range_s;
   __shared__ long long wsum[kWarps + 1];
   volatile int32_t* abort_flag = &abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,27 +321,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
       mbar_init(smem_u32(&empty[s]), 4);
     }
     abort_s = 0;
-    start_s = Start{0, 0, 0, 0};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_launch_dependents();
   __syncthreads();
-  find_range<KT, BM>(a, &total_s, &start_s, wsum);
+  find_range<KT, BM>(a, &range_s, wsum);
   __syncthreads();
-  const int64_t total = total_s;
-  Walk<KT, BM> walk;
-  walk.u = total * blockIdx.x / gridDim.x;
-  walk.u1 = total * (blockIdx.x + 1) / gridDim.x;
-  const int64_t u_first = walk.u;
-  if (threadIdx.x == 0) {
-    Start st = start_s;
-    st.total = total;
-    reinterpret_cast<Start*>(a.ws)[blockIdx.x] = st;
-  }
-  if (walk.u < walk.u1) {
-    walk.base = start_s.base;
-    walk.r = start_s.r;
-    walk.q = request<KT, BM>(a, walk.r);
+  if (range_s.u0 < range_s.u1) {
+    Walk<KT, BM> walk{range_s.u0, range_s.u1, range_s.base, range_s.r, range_s.q};
+    const int64_t u_first = walk.u;
     const int P = 1 << a.page_shift;
     const int PR = P < KT ? P : KT, boxes = KT / PR;  // positions per box, boxes per tile
     const uint32_t all_boxes = (1u << boxes) - 1u;
@@ -559,16 +578,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           } else {
             // slot 0: the CTA's first stretch, when it does not begin the row block; slot 1: the last
             const int64_t begin = walk.u - (s.t1 - s.t0);
-            const int slot = begin == u_first && s.t0 > 0 ? 0 : 1;
-            float* ws = reinterpret_cast<float*>(a.ws + gridDim.x * sizeof(Start)) +
-                        ((int64_t)blockIdx.x * 2 + slot) * BM * (HD + 2);
+            auto* w = piece_of<HD, BM>(a, gridDim.x, blockIdx.x, begin == u_first && s.t0 > 0 ? 0 : 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float* w = ws + (wm * 16 + r0 + 8 * i) * (HD + 2);
-              if ((lane & 3) == 0) *reinterpret_cast<float2*>(w) = make_float2(m[i], l[i]);
+              const int y = wm * 16 + r0 + 8 * i;
+              if ((lane & 3) == 0) w->ml[y] = make_float2(m[i], l[i]);
 #pragma unroll
               for (int d = 0; d < HD / 8; ++d)
-                *reinterpret_cast<float2*>(w + 2 + d * 8 + c0) = make_float2(O[d][2 * i], O[d][2 * i + 1]);
+                reinterpret_cast<float2*>(&w->o[d * 2 + c0 / 4][y])[c0 / 2 & 1] = make_float2(O[d][2 * i], O[d][2 * i + 1]);
             }
           }
         }
@@ -580,53 +597,82 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 }
 
 // Joins the pieces of the row blocks that the CTAs' ranges cut: CTA b looks at
-// the cut at the start of range b, and acts if it is the first of its block.
-// A warp a row, the rows of the block dealt over blockIdx.y.
-template <int HD, int KT, int BM, bool BF>
-__global__ void __launch_bounds__(128) tree_join_kernel(const TreeAttnArgs a) {
+// the cut at the start of range b, and acts if it is the first of its block.  A
+// lane a row, four output columns at a time; the rows and the halves of the
+// columns are dealt over blockIdx.y.
+template <int HD, int BM, bool BF>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeAttnArgs a) {
+  constexpr int RW = BM < 32 ? BM : 32, CW = 32 / RW;  // rows of a warp, column groups it takes at once
+  __shared__ int16_t ids[1024];
+  __shared__ int count;
   pdl_wait();
-  const int G = gridDim.x, b = blockIdx.x;
-  const Start st = reinterpret_cast<const Start*>(a.ws)[b];
-  const int64_t U = st.total;
-  auto first = [&](int64_t c) { return U * c / G; };
-  auto owner = [&](int64_t u) { return (int)(((u + 1) * G - 1) / U); };
-  const int64_t u = first(b);
-  if (b == 0 || u >= first(b + 1)) return;  // an empty range has no cut of its own
-  const Req q = request<KT, BM>(a, st.r);
-  const int64_t item = (u - st.base) / q.tiles, ua = st.base + item * q.tiles, ub = ua + q.tiles;
-  if (u == ua || owner(ua) != owner(u - 1)) return;
-  const int hk = (int)(item / q.blocks), blk = (int)(item - (int64_t)hk * q.blocks), grp = a.H / a.Hk;
-  const int lane = threadIdx.x & 31, rows = min(BM, q.n * grp - blk * BM);
-  const float* ws = reinterpret_cast<const float*>(a.ws + G * sizeof(Start));
-  for (int y = blockIdx.y * 4 + (threadIdx.x >> 5); y < rows; y += gridDim.y * 4) {
-    float m = -INFINITY, l = 0.f, O[HD / 32];
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) O[e] = 0.f;
-    for (int c = owner(ua); c < G;) {
-      const float* w = ws + ((int64_t)c * 2 + (ua < first(c) ? 0 : 1)) * BM * (HD + 2) + y * (HD + 2);
-      const float m2 = w[0], l2 = w[1], mn = fmaxf(m, m2), z = mn == -INFINITY ? 0.f : mn;
-      const float x = ex2(m - z), x2 = ex2(m2 - z);
-      l = l * x + l2 * x2;
-#pragma unroll
-      for (int e = 0; e < HD / 32; ++e) O[e] = O[e] * x + w[2 + e * 32 + lane] * x2;
-      m = mn;
-      if (first(c + 1) >= ub) break;
-      c = owner(first(c + 1));
+  const Range* ranges = reinterpret_cast<const Range*>(a.ws);
+  const int G = gridDim.x, b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Range me = ranges[b];
+  if (me.u0 >= me.u1 || me.u0 == me.ua) return;
+  const int64_t ua = me.ua, ub = me.ub;
+  int p = b - 1;
+  while (ranges[p].u0 >= ranges[p].u1) --p;  // (the block's first unit is in an earlier range)
+  if (ranges[p].u0 > ua) return;             // an earlier cut of the block
+  if (warp == 0) {
+    int n = 1;
+    if (lane == 0) ids[0] = (int16_t)p;
+    for (int c = b + lane;; c += 32) {
+      const bool past = c >= G || ranges[c].u0 >= ub;
+      const bool in = !past && ranges[c].u0 < ranges[c].u1;
+      const unsigned bal = __ballot_sync(0xffffffffu, in);
+      if (in) ids[n + __popc(bal & ((1u << lane) - 1u))] = (int16_t)c;
+      n += __popc(bal);
+      if (__any_sync(0xffffffffu, past)) break;
     }
-    const int rho = blk * BM + y, node = rho / grp, head = hk * grp + rho - node * grp;
-    const int64_t row = q.row0 + node;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) {
-      const float v = O[e] * inv;
-      const int64_t o = row * a.out_stride + (int64_t)head * HD + e * 32 + lane;
-      if (a.out_f32) static_cast<float*>(a.out)[o] = v;
-      else if constexpr (BF) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-      else static_cast<__half*>(a.out)[o] = __float2half_rn(v);
-      if (a.out16) act16_put(a.out16, row, a.H * HD, head * HD + e * 32 + lane, v, a.split16);
-    }
-    if (a.lse && lane == 0) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (lane == 0) count = n;
   }
+  __syncthreads();
+  const int np = count, grp = a.H / a.Hk;
+  const int y = (blockIdx.y >> 1) * RW + lane % RW, rho = me.blk * BM + y;
+  if (rho >= me.q.n * grp) return;
+  const int node = rho / grp, head = me.hk * grp + rho - node * grp;
+  const int64_t row = me.q.row0 + node;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) m = fmaxf(m, piece_of<HD, BM>(a, G, ids[i], i == 0)->ml[y].x);
+  const float z = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) {
+    const float2 ml = piece_of<HD, BM>(a, G, ids[i], i == 0)->ml[y];
+    l += ml.y * ex2(ml.x - z);
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  constexpr int half = HD / 8;  // column groups of a half
+  for (int c = (blockIdx.y & 1) * half + warp * CW + lane / RW; c < ((int)(blockIdx.y & 1) + 1) * half; c += 8 * CW) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const auto* w = piece_of<HD, BM>(a, G, ids[i], i == 0);
+      const float f = ex2(w->ml[y].x - z);
+      const float4 v = w->o[c][y];
+      o.x += f * v.x;
+      o.y += f * v.y;
+      o.z += f * v.z;
+      o.w += f * v.w;
+    }
+    o.x *= inv;
+    o.y *= inv;
+    o.z *= inv;
+    o.w *= inv;
+    const int64_t at = row * a.out_stride + (int64_t)head * HD + c * 4;
+    if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+          make_uint2(pack2<BF>(o.x, o.y), pack2<BF>(o.z, o.w));
+    if (a.out16) {
+      const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) act16_put(a.out16, row, a.H * HD, head * HD + c * 4 + e, v[e], a.split16);
+    }
+  }
+  if (a.lse && blockIdx.y % 2 == 0 && warp == 0 && lane < RW)
+    a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Rows of a block: the smallest that holds a request's rows of a key head.  More than 32 rows of widths 64 and 128
@@ -638,7 +684,7 @@ static int block_rows(int hd, int64_t rows_per_head) {
 }
 
 template <int HD, int KT, int BM, bool BF, class K>
-static int launch(K kern, int threads, int smem, const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms,
+static int launch(K kern, int ctas, int threads, int smem, const TreeAttnArgs& a, const tl_kv_pool& p,
                   cudaStream_t s) {
   constexpr int cols = HD < 64 ? HD : 64;
   CUtensorMap map;
@@ -647,18 +693,18 @@ static int launch(K kern, int threads, int smem, const TreeAttnArgs& a, const tl
                        rows, HD * 2, cols, p.page_tokens < KT ? p.page_tokens : KT,
                        cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
   TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  kern<<<n_sms, threads, smem, s>>>(map, a);
+  kern<<<ctas, threads, smem, s>>>(map, a);
   TL_CUDA(cudaGetLastError());
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(n_sms, BM / 16);
-  lc.blockDim = dim3(128);
+  lc.gridDim = dim3(ctas, 2 * (BM < 32 ? 1 : BM / 32));
+  lc.blockDim = dim3(256);
   lc.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  TL_CUDA(cudaLaunchKernelEx(&lc, tree_join_kernel<HD, KT, BM, BF>, a));
+  TL_CUDA(cudaLaunchKernelEx(&lc, tree_join_kernel<HD, BM, BF>, a));
   return check_cuda(cudaGetLastError());
 }
 
@@ -666,13 +712,14 @@ template <int HD, bool BF>
 static int run(const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms, cudaStream_t s) {
   using C = Cfg<HD>;
   switch (block_rows(HD, (int64_t)a.max_nodes * (a.H / a.Hk))) {
-    case 16: return launch<HD, C::KT, 16, BF>(tree_attn_kernel<HD, 1, BF>, kThreads, C::SMEM, a, p, n_sms, s);
-    case 32: return launch<HD, C::KT, 32, BF>(tree_attn_kernel<HD, 2, BF>, kThreads, C::SMEM, a, p, n_sms, s);
+    case 16: return launch<HD, C::KT, 16, BF>(tree_attn_kernel<HD, 1, BF>, n_sms, kThreads, C::SMEM, a, p, s);
+    case 32: return launch<HD, C::KT, 32, BF>(tree_attn_kernel<HD, 2, BF>, n_sms, kThreads, C::SMEM, a, p, s);
     default:
       if constexpr (HD == 32)
-        return launch<HD, C::KT, 64, BF>(tree_attn_kernel<HD, 4, BF>, kThreads, C::SMEM, a, p, n_sms, s);
+        return launch<HD, C::KT, 64, BF>(tree_attn_kernel<HD, 4, BF>, n_sms, kThreads, C::SMEM, a, p, s);
       else
-        return launch<HD, 128, 128, BF>(tree_attn_tc_kernel<HD, BF>, 256, TcCfg<HD>::SMEM, a, p, n_sms, s);
+        return launch<HD, TcCfg<HD>::KT, 128, BF>(tree_attn_tc_kernel<HD, BF>, 2 * n_sms, TcCfg<HD>::THREADS,
+                                                  TcCfg<HD>::SMEM, a, p, s);
   }
 }
 
@@ -686,7 +733,9 @@ static int sm_count(int* n) {
 }  // namespace tree
 
 size_t tree_attn_workspace(int hd, int64_t rows_per_head, int n_sms) {
-  return (size_t)n_sms * sizeof(tree::Start) + (size_t)n_sms * 2 * tree::block_rows(hd, rows_per_head) * (hd + 2) * 4;
+  const int rows = tree::block_rows(hd, rows_per_head);
+  const size_t ctas = (size_t)n_sms * (rows == 128 ? 2 : 1);
+  return (ctas * sizeof(tree::Range) + 255) / 256 * 256 + ctas * 2 * rows * (hd + 2) * 4;
 }
 
 int tree_attn_run(TreeAttnArgs a, const tl_kv_pool& p, cudaStream_t s, int64_t* launches) {

@@ -2,12 +2,11 @@
 // blocks of more rows than the warp-level matrix instructions keep up with.
 // Same units, ranges, pieces and page handling as tree_attn_kernel.
 //
-// One CTA per SM; a row block is 128 query rows (one TMEM lane, one thread
-// each), a tile 128 key positions:
+// A row block is 128 query rows (one TMEM lane and one thread each), a tile 64
+// key positions:
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, into one of two
-//                  TMEM buffers, so the next tile's product runs under this
-//                  tile's softmax
-//   P = exp2(S-m)  one thread a row; 16-bit P replaces S in its TMEM buffer
+//                  TMEM buffers
+//   P = exp2(S-m)  one thread a row; 16-bit P replaces S in its TMEM columns
 //   O += P V       tcgen05.mma with P as the TMEM operand A and V (rows of
 //                  keys) as the N-major operand B, accumulating in TMEM
 // The reference m of a row moves only when a tile's maximum passes it by more
@@ -15,10 +14,17 @@
 // fp32), so O is rescaled in TMEM a few times per row block instead of once
 // per tile.
 //
-// Warp 0: TMA producer; warp 1: MMA issuer; warp 2: TMEM; warps 4-7: rows.
-// Bound by the cache's bytes up to 128 rows: 128 positions of width 128 are
-// 64 KB (about 2,800 cycles of one SM's share of HBM) against 16 MMAs of
-// 128 x 128 x 16 and 128 exponentials a thread.
+// Two CTAs an SM, each with half of shared memory and TMEM: one streams while
+// the other is between row blocks (the last tile's masks, the output, the next
+// queries: some 25,000 cycles where 25 tiles of 128 positions take 70,000).
+// With one CTA of 128-position tiles and three rings of buffers the same
+// 64 requests x 32 nodes x 4 heads on 4,000 positions took 252-259 us.
+//
+// Warp 0 loads K, warp 2 loads V (each its own ring), warp 1 issues Q K^T, warp
+// 3 issues P V, so no one of them waits for another's turn; warps 4-7: rows.
+// Bound by the cache's bytes up to 128 rows: 64 positions of width 128 are
+// 32 KB (about 1,400 cycles of one SM's share of HBM) against 12 MMAs and 64
+// exponentials a thread (512 cycles of the SM's).
 #pragma once
 
 #include "ptx.cuh"
@@ -28,17 +34,18 @@ namespace tree {
 
 template <int HD>
 struct TcCfg {
-  static constexpr int KT = 128, BM = 128;
+  static constexpr int KT = 64, BM = 128;
   static constexpr int CT = HD / 64;               // 64-wide column tiles
-  static constexpr int TILE = KT * 128;            // bytes of one: [128 positions x 64] 16 bit
-  static constexpr int STAGE = 2 * CT * TILE;      // K tiles, then V tiles
-  static constexpr int STAGES = HD == 128 ? 3 : 6;
+  static constexpr int TILE = KT * 128;            // bytes of one: [64 positions x 64] 16 bit
+  static constexpr int STAGE = CT * TILE;          // K or V of a tile
+  static constexpr int STAGES = HD == 128 ? 2 : 4; // of K, and of V
   static constexpr int Q_BYTES = BM * HD * 2;
-  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * STAGE + 256;
-  static constexpr int TMEM_COLS = 512;            // S / P twice 128, O HD
-  static_assert(SMEM <= 227 * 1024, "tile ring does not fit");
-  // a second CTA on the SM would wait for TMEM that the first holds: the ring leaves no room for one
-  static_assert(SMEM > 114 * 1024, "one CTA per SM");
+  static constexpr int SB = 2;                     // S buffers
+  static constexpr int TMEM_COLS = 256;            // S / P twice 64, O HD
+  static constexpr int THREADS = 256;
+  static constexpr int SMEM = 1024 + Q_BYTES + 2 * STAGES * STAGE + 512;
+  // two CTAs share an SM (and its 512 columns of TMEM), never three
+  static_assert(SMEM <= 113 * 1024 && SMEM > 76 * 1024, "two CTAs per SM");
 };
 
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {  // 128-byte swizzle
@@ -95,7 +102,18 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// Whether any of the 128 row threads says so (all of them call it).
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Barrier 1: the 128 row threads.
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Whether any row thread says so (all of them call it).
 __device__ __forceinline__ bool rows_any(bool v) {
   uint32_t r;
   asm volatile(
@@ -107,13 +125,67 @@ __device__ __forceinline__ bool rows_any(bool v) {
   return r != 0;
 }
 
+// Tiles whose boxes are remembered: K runs at most STAGES tiles ahead of S, and S three ahead of the rows.
+constexpr int kInfo = 16;
+
+// A producer warp: K or V of the tiles of the CTA's range into its ring, a box
+// per page (or part of one).
+template <class C>
+__device__ __forceinline__ void produce_half(const TreeAttnArgs& a, const CUtensorMap& kvmap, Walk<C::KT, C::BM> walk,
+                                             bool values, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                             volatile uint32_t* info, volatile int32_t* abort_flag) {
+  constexpr int KT = C::KT;
+  const int lane = threadIdx.x & 31;
+  const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR;
+  Seg s;
+  int k = 0;
+  bool ok = true;
+  while (ok && walk.next(a, s)) {
+    const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
+    const int64_t head = (int64_t)s.hk + (values ? a.Hk : 0);
+    auto page_of = [&](int t) {
+      const int pos = t * KT + lane * PR;
+      return lane < boxes && pos < s.q.len ? __ldg(table + (pos >> a.page_shift)) : -1;
+    };
+    int page = page_of(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++k) {
+      const int next_page = t + 1 < s.t1 ? page_of(t + 1) : -1;
+      const int st = k % C::STAGES, round = k / C::STAGES;
+      if (round > 0 && !mbar_wait_warp(smem_u32(&empty[st]), (round - 1) & 1, abort_flag)) { ok = false; break; }
+      const int pos = t * KT + lane * PR;
+      const bool want = lane < boxes && pos < s.q.len;
+      const bool good = want && page >= 0 && page < a.n_pages;
+      if (want && !good && a.status) atomicOr(a.status, TL_BAD_PAGE);
+      const uint32_t in = __ballot_sync(0xffffffffu, good);
+      const uint32_t bar = smem_u32(&full[st]);
+      if (lane == 0) {
+        if (!values) info[k % kInfo] = in;
+        mbar_expect_tx(bar, __popc(in) * C::CT * PR * 128);
+      }
+      __syncwarp();
+      if (good) {
+        const int64_t y = (((int64_t)page * 2 * a.Hk + head) << a.page_shift) + (pos & (P - 1));
+        const uint32_t dst = smem_u32(ring + st * C::STAGE) + lane * PR * 128;
+#pragma unroll
+        for (int ct = 0; ct < C::CT; ++ct) tma_load_2d(dst + ct * C::TILE, &kvmap, ct * 64, (int)y, bar);
+      }
+      __syncwarp();
+      page = next_page;
+    }
+  }
+  if (!ok && lane == 0) {  // let the copies in flight land
+    volatile int32_t never = 0;
+    for (int i = k > C::STAGES ? k - C::STAGES : 0; i < k; ++i)
+      mbar_wait(smem_u32(&full[i % C::STAGES]), (i / C::STAGES) & 1, &never);
+  }
+}
+
 // Bits of the 32 positions from p0 on that a row sees.
-__device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q, int64_t row, int node, int p0,
-                                             uint32_t landed, int PR, int tile_off) {
+__device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q, int64_t row, int node, int p0) {
   auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
   const int j0 = p0 - q.ctx;  // node index of the first position
   uint32_t v = low(-j0);      // the context
-  if (j0 > -32 && node >= 0) {
+  if (j0 > -32) {
     if (a.masks) {
       const uint32_t* w = a.masks + row * a.words;
       auto word = [&](int i) { return i >= 0 && i < a.words ? __ldg(w + i) : 0u; };
@@ -122,45 +194,90 @@ __device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q
       v |= low(node + 1 - j0) & ~low(-j0);
     }
   }
-  const uint32_t lo = landed >> (tile_off / PR) & 1u, hi = landed >> ((tile_off + 16) / PR) & 1u;
-  return v & low(q.len - p0) & ((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
+  return v & low(q.len - p0);
+}
+
+// Sums p * v of the values of 64 positions that are not finite, over the positions with a probability.
+template <int HD, bool BF>
+__device__ __noinline__ void add_odd(const float* p, const uint8_t* vt, float* add) {
+  constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
+  for (int d = 0; d < HD; ++d) add[d] = 0.f;
+  for (int y = 0; y < 64; ++y) {
+    if (p[y] == 0.f) continue;
+    for (int d = 0; d < HD; ++d) {
+      const int r = y, c = d / 8;
+      const uint32_t b = *reinterpret_cast<const uint16_t*>(vt + (c / 8) * TcCfg<HD>::TILE + r * 128 +
+                                                            (((c % 8) ^ (r & 7)) << 4) + (d % 8) * 2);
+      if ((b & X) == X) add[d] += p[y] * unpack2<BF>(b).x;
+    }
+  }
+}
+// Adds HD values to the thread's row of O.
+template <int HD>
+__device__ __noinline__ void add_to_o(uint32_t to, const float* add) {
+  for (int c = 0; c < HD; c += 32) {
+    float o[32];
+    tc_ld32(to + c, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] += add[c + i];
+    tc_st32(to + c, reinterpret_cast<const uint32_t*>(o));
+  }
+  tc_wait_st();
+}
+
+// Scales the thread's row of O.
+template <int HD>
+__device__ __noinline__ void scale_o(uint32_t to, float f) {
+#pragma unroll 1
+  for (int c = 0; c < HD; c += 32) {
+    float o[32];
+    tc_ld32(to + c, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= f;
+    tc_st32(to + c, reinterpret_cast<const uint32_t*>(o));
+  }
+  tc_wait_st();
 }
 
 template <int HD, bool BF>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(TcCfg<HD>::THREADS, 2)
 tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
   using C = TcCfg<HD>;
-  constexpr int KT = C::KT, BM = C::BM, ST = C::STAGES;
+  constexpr int KT = C::KT, BM = C::BM, ST = C::STAGES, SB = C::SB;
   extern __shared__ __align__(1024) uint8_t smem_tt[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_tt) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = sQ + C::Q_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * C::STAGE);
-  uint64_t* empty = full + ST;
-  uint64_t* s_full = empty + ST;   // [2] S of a tile in TMEM
-  uint64_t* p_full = s_full + 2;   // [2] P of a tile in TMEM, V clean
-  uint64_t* o_full = p_full + 2;   // [2] P V of a tile added
-  uint64_t* q_full = o_full + 2;   // Q of a row block in shared memory
-  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(q_full + 1);  // [ST] boxes that landed
-  __shared__ int32_t abort_s;
-  __shared__ uint32_t tmem_s;
-  __shared__ int64_t total_s;
-  __shared__ Start start_s;
-  __shared__ long long wsum[8];
-  volatile int32_t* abort_flag = &abort_s;
+  uint8_t* ring_k = sQ + C::Q_BYTES;
+  uint8_t* ring_v = ring_k + ST * C::STAGE;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(ring_v + ST * C::STAGE);
+  uint64_t* k_empty = k_full + ST;
+  uint64_t* v_full = k_empty + ST;
+  uint64_t* v_empty = v_full + ST;
+  uint64_t* s_full = v_empty + ST;  // [SB] S of a tile in TMEM
+  uint64_t* p_full = s_full + SB;   // [SB] P of a tile in TMEM, V clean
+  uint64_t* o_full = p_full + SB;   // [SB] P V of a tile added
+  uint64_t* q_full = o_full + SB;   // Q of a row block in shared memory
+  Range& range_s = *reinterpret_cast<Range*>(q_full + 1);
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(&range_s + 1);  // [kInfo] boxes in the pool
+  uint32_t& tmem_s = *const_cast<uint32_t*>(info + kInfo);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(&tmem_s + 1);
+  long long* wsum = reinterpret_cast<long long*>(sQ);  // before any Q
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&k_full[s]), 1);
+      mbar_init(smem_u32(&k_empty[s]), 1);
+      mbar_init(smem_u32(&v_full[s]), 1);
+      mbar_init(smem_u32(&v_empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < SB; ++b) {
       mbar_init(smem_u32(&s_full[b]), 1);
       mbar_init(smem_u32(&p_full[b]), 4);
       mbar_init(smem_u32(&o_full[b]), 1);
     }
     mbar_init(smem_u32(q_full), 4);
-    abort_s = 0;
-    start_s = Start{0, 0, 0, 0};
+    *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
@@ -173,84 +290,84 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
   tc_before();
   __syncthreads();
   tc_after();
-  find_range<KT, BM>(a, &total_s, &start_s, wsum);
+  find_range<KT, BM>(a, &range_s, wsum);
   __syncthreads();
   const uint32_t tmem = tmem_s;
-  const int64_t total = total_s;
-  Walk<KT, BM> walk;
-  walk.u = total * blockIdx.x / gridDim.x;
-  walk.u1 = total * (blockIdx.x + 1) / gridDim.x;
+  Walk<KT, BM> walk{range_s.u0, range_s.u1, range_s.base, range_s.r, range_s.q};  // nothing where u0 == u1
   const int64_t u_first = walk.u;
-  if (threadIdx.x == 0) {
-    Start st = start_s;
-    st.total = total;
-    reinterpret_cast<Start*>(a.ws)[blockIdx.x] = st;
-  }
-  if (walk.u < walk.u1 && warp != 2 && warp != 3) {
-    walk.base = start_s.base;
-    walk.r = start_s.r;
-    walk.q = request<KT, BM>(a, walk.r);
-    const int P = 1 << a.page_shift;
-    const int PR = P < KT ? P : KT, boxes = KT / PR;
-    const uint32_t all_boxes = (1u << boxes) - 1u;
-    Seg s;
-    int k = 0;  // tiles of this CTA so far
-    if (warp == 0) {
-      produce<C, KT, BM>(a, kvmap, walk, ring, full, empty, info, abort_flag);
+  Seg s;
+  int k = 0;  // tiles of this CTA so far
+  if (warp < 4) {
+    if (warp == 0 || warp == 2) {
+      produce_half<C>(a, kvmap, walk, warp == 2, warp == 0 ? ring_k : ring_v, warp == 0 ? k_full : v_full,
+                      warp == 0 ? k_empty : v_empty, info, abort_flag);
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t id_s = tc_idesc(BF, KT, 0), id_o = tc_idesc(BF, HD, 1);
+      // ------------------------------------------------------------- S = Q K^T
+      constexpr uint32_t idesc = tc_idesc(BF, KT, 0);
       bool ok = true;
-      auto issue_s = [&](int kk) {
-        const int st = kk % ST;
-        if (!mbar_wait_warp(smem_u32(&full[st]), (kk / ST) & 1, abort_flag)) return false;
-        tc_after();
-        const uint8_t* kt = ring + st * C::STAGE;
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i)
-            tc_mma_ss(tmem + (kk & 1) * KT, tc_desc(smem_u32(sQ + (i / 4) * (BM * 128)) + (i % 4) * 32, 16, 1024),
-                      tc_desc(smem_u32(kt + (i / 4) * C::TILE) + (i % 4) * 32, 16, 1024), id_s, i > 0);
-          tc_commit(smem_u32(&s_full[kk & 1]));
-        }
-        __syncwarp();
-        return true;
-      };
       for (int seg = 0; ok && walk.next(a, s); ++seg) {
         if (!(ok = mbar_wait_warp(smem_u32(q_full), seg & 1, abort_flag))) break;
-        tc_after();
-        if (!(ok = issue_s(k))) break;
         for (int t = s.t0; t < s.t1; ++t, ++k) {
-          if (t + 1 < s.t1 && !(ok = issue_s(k + 1))) break;
-          if (!(ok = mbar_wait_warp(smem_u32(&p_full[k & 1]), (k >> 1) & 1, abort_flag))) break;
+          const int st = k % ST, buf = k % SB;
+          // P of tile k - 2 has been read from this buffer
+          ok = (k < SB || mbar_wait_warp(smem_u32(&o_full[buf]), (k / SB - 1) & 1, abort_flag)) &&
+               mbar_wait_warp(smem_u32(&k_full[st]), (k / ST) & 1, abort_flag);
+          if (!ok) break;
           tc_after();
-          const int st = k % ST;
-          const uint8_t* vt = ring + st * C::STAGE + C::CT * C::TILE;
+          const uint8_t* kt = ring_k + st * C::STAGE;
           if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < KT / 16; ++i)
-              // V: rows of keys, 64 values of N per 128-byte row; 8-key groups 1024 B apart, the next 64 of N one
-              // column tile further
-              tc_mma_ts(tmem + 2 * KT, tmem + (k & 1) * KT + i * 8, tc_desc(smem_u32(vt) + i * 16 * 128, C::TILE, 1024),
-                        id_o, t > s.t0 || i > 0);
-            tc_commit(smem_u32(&o_full[k & 1]));
-            tc_commit(smem_u32(&empty[st]));
+            for (int i = 0; i < HD / 16; ++i)
+              tc_mma_ss(tmem + buf * KT, tc_desc(smem_u32(sQ + (i / 4) * (BM * 128)) + (i % 4) * 32, 16, 1024),
+                        tc_desc(smem_u32(kt + (i / 4) * C::TILE) + (i % 4) * 32, 16, 1024), idesc, i > 0);
+            tc_commit(smem_u32(&s_full[buf]));
+            tc_commit(smem_u32(&k_empty[st]));
           }
           __syncwarp();
         }
       }
     } else {
+      // --------------------------------------------------------------- O += P V
+      constexpr uint32_t idesc = tc_idesc(BF, HD, 1);
+      bool ok = true;
+      while (ok && walk.next(a, s)) {
+        for (int t = s.t0; t < s.t1; ++t, ++k) {
+          const int st = k % ST, buf = k % SB;
+          ok = mbar_wait_warp(smem_u32(&v_full[st]), (k / ST) & 1, abort_flag) &&
+               mbar_wait_warp(smem_u32(&p_full[buf]), (k / SB) & 1, abort_flag);
+          if (!ok) break;
+          tc_after();
+          const uint8_t* vt = ring_v + st * C::STAGE;
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i)
+              // V: rows of keys, 64 values of N per 128-byte row; 8-key groups 1024 B apart, the next 64 of N one
+              // column tile further
+              tc_mma_ts(tmem + SB * KT, tmem + buf * KT + i * 8,
+                        tc_desc(smem_u32(vt) + i * 16 * 128, C::TILE, 1024), idesc, t > s.t0 || i > 0);
+            tc_commit(smem_u32(&o_full[buf]));
+            tc_commit(smem_u32(&v_empty[st]));
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else {
+    {
       // ------------------------------------------------------------------ rows
       const int t_row = threadIdx.x - 128;
-      const uint32_t tl = tmem + ((uint32_t)((warp - 4) * 32) << 16);  // the warp's TMEM lanes
+      const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // the warp's TMEM lanes
+      const uint32_t to = tl + SB * KT;
       const int G = a.H / a.Hk;
+      const int PR = min(1 << a.page_shift, KT);
+      const uint32_t all_boxes = (1u << (KT / PR)) - 1u;
       bool ok = true;  // once a wait ran out: no more waits or TMEM, but every barrier of the rows is still met
       while (walk.next(a, s)) {
-        const Req& q = s.q;
+        const int ctx = s.q.ctx, len = s.q.len;
         const int rho = s.blk * BM + t_row;
-        const bool valid = rho < q.n * G;
+        const bool valid = rho < s.q.n * G;
         const int node = valid ? rho / G : -1, head = s.hk * G + (valid ? rho - node * G : 0);
-        const int64_t row = q.row0 + (valid ? node : 0);
+        const int64_t row = s.q.row0 + (valid ? node : 0);
         const bool active = __any_sync(0xffffffffu, valid);
         if (ok) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_stride +
@@ -266,52 +383,52 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
         }
         float m = -INFINITY, l = 0.f;
         for (int t = s.t0; t < s.t1; ++t, ++k) {
-          const int buf = k & 1, st = k % ST;
-          const bool nodes_here = (t + 1) * KT > q.ctx;
-          ok = ok && mbar_wait_warp(smem_u32(&s_full[buf]), (k >> 1) & 1, abort_flag) &&
-               mbar_wait_warp(smem_u32(&full[st]), (k / ST) & 1, abort_flag);
+          const int st = k % ST, buf = k % SB;
+          const bool nodes_here = (t + 1) * KT > ctx;
+          uint32_t see[2] = {0u, 0u};
+          if (nodes_here && valid) {  // on their way while the product runs
+            see[0] = row_sees(a, s.q, row, node, t * KT);
+            see[1] = row_sees(a, s.q, row, node, t * KT + 32);
+          }
+          ok = ok && mbar_wait_warp(smem_u32(&s_full[buf]), (k / SB) & 1, abort_flag);
+          const uint32_t landed = ok ? info[k % kInfo] : 0u;
+          const bool mask = landed != all_boxes || nodes_here;
+          if (ok && mask) ok = mbar_wait_warp(smem_u32(&v_full[st]), (k / ST) & 1, abort_flag);
           if (!ok) {
-            if (nodes_here && rows_any(false)) asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (nodes_here && rows_any(false)) rows_sync();
             continue;
           }
           tc_after();
-          const uint32_t landed = info[st];
-          const bool mask = landed != all_boxes || nodes_here;
+          const uint32_t ts = tl + buf * KT;
+          uint8_t* vt = ring_v + st * C::STAGE;
           float sv[KT];
           if (active) {
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c) tc_ld32(tl + buf * KT + 32 * c, sv + 32 * c);
+            tc_ld32(ts, sv);
+            tc_ld32(ts + 32, sv + 32);
             tc_wait_ld();
             if (mask) {
 #pragma unroll
-              for (int c = 0; c < KT / 32; ++c) {
-                const uint32_t v = valid ? row_sees(a, q, row, node, t * KT + 32 * c, landed, PR, 32 * c) : 0u;
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t lo = landed >> (32 * c / PR) & 1u, hi = landed >> ((32 * c + 16) / PR) & 1u;
+                const uint32_t v = (nodes_here ? see[c] : 0xffffffffu) & ((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sv[32 * c + i] = v >> i & 1u ? sv[32 * c + i] : -INFINITY;
               }
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-            for (int i = 0; i < KT; i += 8)
+            for (int i = 4; i < KT; i += 4)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(sv[i + e], sv[i + 4 + e]));
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[i + e]);
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             // the row's reference: the first tile's maximum, and a new one only past 2^8 times it
             const bool move = mt > (t == s.t0 ? m : m + 8.f);
             const float mn = move ? mt : m, z = mn == -INFINITY ? 0.f : mn;
             if (t > s.t0 && __any_sync(0xffffffffu, move)) {
               const float corr = move ? ex2(m - z) : 1.f;
-              ok = mbar_wait_warp(smem_u32(&o_full[buf ^ 1]), ((k - 1) >> 1) & 1, abort_flag);
+              ok = mbar_wait_warp(smem_u32(&o_full[buf ^ 1]), ((k - 1) / SB) & 1, abort_flag);
               tc_after();
-#pragma unroll
-              for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                tc_ld32(tl + 2 * KT + 32 * c, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= corr;
-                tc_st32(tl + 2 * KT + 32 * c, reinterpret_cast<const uint32_t*>(o));
-              }
+              scale_o<HD>(to, corr);
               l *= corr;
             }
             m = mn;
@@ -322,145 +439,118 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
             for (int i = 0; i < KT; i += 2) {
               float x, y;
               f2_out(fma2(f2(sv[i], sv[i + 1]), sc, mz), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              sv[i] = x;
-              sv[i + 1] = y;
-              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], f2(x, y));
+              sv[i] = ex2(x);
+              sv[i + 1] = ex2(y);
+              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], f2(sv[i], sv[i + 1]));
               // one rounding of each probability to the values' type (the matrix instruction takes one type)
-              pk[i / 2] = pack2<BF>(x, y);
+              pk[i / 2] = pack2<BF>(sv[i], sv[i + 1]);
             }
+            tc_st32(ts, pk);
             float s0, s1;
             f2_out(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
-            tc_st32(tl + buf * KT, pk);
-            tc_st32(tl + buf * KT + 32, pk + 32);
             tc_wait_st();
           }
           bool odd = false;
           if (mask) {
-            // Values of positions that nobody sees may be anything, and 0 * NaN is not 0.  Thread y looks after
-            // position y of the tile.
-            const int pos = t * KT + t_row;
-            uint8_t* vt = ring + st * C::STAGE + C::CT * C::TILE;
-            bool mine = false;
-            auto chunk = [&](int y, int c) {
+            // Values of positions that nobody sees may be anything, and 0 * NaN is not 0.  Two threads look after a
+            // position of the tile.
+            constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
+            const int y = t_row & 63, pos = t * KT + y, c0 = (t_row >> 6) * (HD / 16);
+            auto chunk = [&](int c) {  // 8 of its values
               return reinterpret_cast<uint4*>(vt + (c / 8) * C::TILE + y * 128 + (((c % 8) ^ (y & 7)) << 4));
             };
-            constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
-            if (pos >= q.len || !(landed >> (t_row / PR) & 1u)) {
+            bool mine = false;
+            if (pos >= len || !(landed >> (y / PR) & 1u)) {
 #pragma unroll
-              for (int c = 0; c < HD / 8; ++c) *chunk(t_row, c) = make_uint4(0, 0, 0, 0);
-            } else if (pos >= q.ctx && (q.n > 1 || a.masks)) {
+              for (int c = 0; c < HD / 16; ++c) *chunk(c0 + c) = make_uint4(0, 0, 0, 0);
+            } else if (pos >= ctx && (s.q.n > 1 || a.masks)) {
 #pragma unroll
-              for (int c = 0; c < HD / 8; ++c) {
-                const uint4 w = *chunk(t_row, c);
+              for (int c = 0; c < HD / 16; ++c) {
+                const uint4 w = *chunk(c0 + c);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mine |= (u[e] & X) == X || (u[e] >> 16 & X) == X;
               }
             }
-            if (nodes_here) {  // have all rows agree on whether a value is not finite
-              odd = rows_any(mine);
-              if (odd) {
-                // the values that are not finite enter by hand, where the row sees the position, and as 0 in P V
-                float add[HD], pl[KT];
+            if (nodes_here) odd = rows_any(mine);
+            if (odd) {
+              // the values that are not finite enter by hand, where the row sees the position, and as 0 in P V
+              float add[HD], pl[KT];
 #pragma unroll
-                for (int d = 0; d < HD; ++d) add[d] = 0.f;
+              for (int i = 0; i < KT; ++i) pl[i] = active ? sv[i] : 0.f;
+              add_odd<HD, BF>(pl, vt, add);
+              rows_sync();
+              if (mine) {
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                  uint32_t* u = reinterpret_cast<uint32_t*>(chunk(c0 + c));
 #pragma unroll
-                for (int i = 0; i < KT; ++i) pl[i] = active ? sv[i] : 0.f;
-#pragma unroll 1
-                for (int y = 0; y < KT; ++y)
-#pragma unroll 1
-                  for (int c = 0; c < HD / 8; ++c) {
-                    const uint4 w = *chunk(y, c);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll 1
-                    for (int e = 0; e < 8; ++e) {
-                      const uint32_t b = u[e >> 1] >> (16 * (e & 1)) & 0xffffu;
-                      const float2 v = unpack2<BF>(b);
-                      if ((b & X) == X && pl[y] != 0.f) add[c * 8 + e] += pl[y] * v.x;
-                    }
+                  for (int e = 0; e < 4; ++e) {
+                    if ((u[e] & X) == X) u[e] &= 0xffff0000u;
+                    if ((u[e] >> 16 & X) == X) u[e] &= 0xffffu;
                   }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (mine)
-#pragma unroll 1
-                  for (int c = 0; c < HD / 8; ++c) {
-                    uint32_t* u = reinterpret_cast<uint32_t*>(chunk(t_row, c));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      if ((u[e] & X) == X) u[e] &= 0xffff0000u;
-                      if ((u[e] >> 16 & X) == X) u[e] &= 0xffffu;
-                    }
-                  }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
-                ok = ok && mbar_wait_warp(smem_u32(&o_full[buf]), (k >> 1) & 1, abort_flag);
-                tc_after();
-#pragma unroll
-                for (int c = 0; c < HD / 32; ++c) {
-                  float o[32];
-                  tc_ld32(tl + 2 * KT + 32 * c, o);
-                  tc_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] += add[32 * c + i];
-                  tc_st32(tl + 2 * KT + 32 * c, reinterpret_cast<const uint32_t*>(o));
                 }
-                tc_wait_st();
               }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              tc_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+              ok = ok && mbar_wait_warp(smem_u32(&o_full[buf]), (k / SB) & 1, abort_flag);
+              tc_after();
+              add_to_o<HD>(to, add);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before P V reads them
           }
           if (!odd) {
+            if (mask) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before P V reads them
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
           }
         }
-        // ------------------------------------------------ the row block's end
-        ok = ok && mbar_wait_warp(smem_u32(&o_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort_flag);
-        if (!ok) continue;
+        // ---------------------------------------------- the row block's end
+        ok = ok && mbar_wait_warp(smem_u32(&o_full[(k - 1) % SB]), ((k - 1) / SB) & 1, abort_flag);
         tc_after();
-        const bool whole = s.t0 == 0 && s.t1 == q.tiles;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        float* ws = reinterpret_cast<float*>(a.ws + gridDim.x * sizeof(Start)) +
-                    ((int64_t)blockIdx.x * 2 + (walk.u - (s.t1 - s.t0) == u_first && s.t0 > 0 ? 0 : 1)) * BM * (HD + 2) +
-                    t_row * (HD + 2);
-        if (active) {
+        if (active && ok) {
+          const bool whole = s.t0 == 0 && s.t1 == s.q.tiles;
+          const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+          auto* w = piece_of<HD, BM>(a, gridDim.x, blockIdx.x, walk.u - (s.t1 - s.t0) == u_first && s.t0 > 0 ? 0 : 1);
 #pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
+          for (int c0 = 0; c0 < HD; c0 += 32) {
             float o[32];
-            tc_ld32(tl + 2 * KT + 32 * c, o);
+            tc_ld32(to + c0, o);
             tc_wait_ld();
             if (!valid) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
             if (whole) {
-              const int64_t at = row * a.out_stride + (int64_t)head * HD + 32 * c;
+              const int64_t at = row * a.out_stride + (int64_t)head * HD + c0;
               if (a.out_f32) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                   *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + i) =
-                      make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                      make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; i += 8)
                   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + i) =
-                      make_uint4(pack2<BF>(o[i] * inv, o[i + 1] * inv), pack2<BF>(o[i + 2] * inv, o[i + 3] * inv),
-                                 pack2<BF>(o[i + 4] * inv, o[i + 5] * inv), pack2<BF>(o[i + 6] * inv, o[i + 7] * inv));
+                      make_uint4(pack2<BF>(o[i], o[i + 1]), pack2<BF>(o[i + 2], o[i + 3]),
+                                 pack2<BF>(o[i + 4], o[i + 5]), pack2<BF>(o[i + 6], o[i + 7]));
               }
               if (a.out16)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  act16_put(a.out16, row, a.H * HD, head * HD + 32 * c + i, o[i] * inv, a.split16);
+                  act16_put(a.out16, row, a.H * HD, head * HD + c0 + i, o[i], a.split16);
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                *reinterpret_cast<float2*>(ws + 2 + 32 * c + i) = make_float2(o[i], o[i + 1]);
+              for (int i = 0; i < 32; i += 4)
+                w->o[(c0 + i) / 4][t_row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
-          if (valid && whole && a.lse) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-          if (valid && !whole) *reinterpret_cast<float2*>(ws) = make_float2(m, l);
+          if (valid) {
+            if (whole && a.lse) a.lse[row * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (!whole) w->ml[t_row] = make_float2(m, l);
+          }
         }
         tc_before();
       }
@@ -468,7 +558,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
   }
   tc_before();
   __syncthreads();
-  if (threadIdx.x == 0 && abort_s && a.status) atomicOr(a.status, TL_TIMED_OUT);
+  if (threadIdx.x == 0 && *abort_flag && a.status) atomicOr(a.status, TL_TIMED_OUT);
   if (warp == 2) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::TMEM_COLS)
