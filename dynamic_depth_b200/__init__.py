@@ -164,6 +164,34 @@ class LoopedLM:
                                  C.byref(rounds)), "tl_speculate")
         return tok, rounds.value
 
+    def speculate_tree(self, lane: int, n_new: int, L_draft: int, L_verify: int, widths):
+        """speculate() with a tree of drafts, widths[i] children for each node of level i:
+        (tokens int32 [n_new], verify rounds)."""
+        w = np.ascontiguousarray(widths, dtype=np.int32)
+        tok = np.zeros(n_new, np.int32)
+        rounds = C.c_int32(0)
+        check(lib().tl_speculate_tree(self.h, lane, n_new, L_draft, L_verify, w.ctypes.data, len(w), tok.ctypes.data,
+                                      C.byref(rounds)), "tl_speculate_tree")
+        return tok, rounds.value
+
+    def score(self, lane: int, tokens, L: int, n_top: int = 0, share_from: int = -1, shared_tokens: int = 0):
+        """Prefill a lane and score its tokens: a TokenLogprobs of device tensors, one row per position computed
+        (the last position has no target)."""
+        from .ops import TokenLogprobs
+        tok = np.ascontiguousarray(tokens, dtype=np.int32)
+        torch, T = self.torch, len(tok)
+        with torch.cuda.stream(self.stream):
+            lp, ent, lse = (torch.empty(T, dtype=torch.float32, device=self.device) for _ in range(3))
+            rank = torch.empty(T, dtype=torch.int32, device=self.device)
+            ids = torch.empty((T, n_top), dtype=torch.int32, device=self.device) if n_top else None
+            top = torch.empty((T, n_top), dtype=torch.float32, device=self.device) if n_top else None
+        rows = C.c_int32(0)
+        check(lib().tl_score(self.h, lane, tok.ctypes.data, T, L, share_from, shared_tokens, n_top, _ptr(lp),
+                             _ptr(rank), _ptr(ent), _ptr(lse), _ptr(ids), _ptr(top), C.byref(rows)), "tl_score")
+        n = rows.value
+        return TokenLogprobs(lp[:n], rank[:n], ent[:n], lse[:n], ids[:n] if n_top else None,
+                             top[:n] if n_top else None)
+
     def set_tick_overlap(self, mode: int):
         """0 automatic, 1 entering lanes iterate in the boundary stage, 2 they join at the next tick,
         3 boundary stages and loop steps on two streams with no join per tick."""

@@ -71,6 +71,10 @@ SIGNATURES = {
                               C.c_void_p]),
     "tl_speculate": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
                                C.c_void_p]),
+    "tl_speculate_tree": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int32,
+                                    C.c_void_p, C.c_void_p]),
+    "tl_score": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                           C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "tl_set_tick_overlap": (C.c_int, [C.c_void_p, C.c_int32]),
     "tl_set_cascade": (C.c_int, [C.c_void_p, C.c_int32]),
     "tl_set_graphs": (C.c_int, [C.c_void_p, C.c_int32]),

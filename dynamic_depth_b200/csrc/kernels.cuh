@@ -1008,6 +1008,31 @@ __global__ void release_rows_kernel(Rows rows, LaneState* lanes) {
   phase_release(&lanes[rows.lane[r]].phase, PH_LOOP);
 }
 
+// Keys and values of a kept tree path to consecutive positions: position
+// pos0 + path[i] of every cache slot below gridDim.x moves to pos0 + i.  path
+// ascends and path[i] >= i, so no position is read after it was written.  One
+// CTA a (cache slot, head).
+__global__ void tree_path_kernel(KVGeom g, int lane, int pos0, const int32_t* __restrict__ path, int n,
+                                 int32_t* __restrict__ status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int slot = blockIdx.x, h = blockIdx.y;
+  const int64_t v_off = (int64_t)g.H * g.page_tokens * g.hd;
+  for (int i = 1; i < n; ++i) {
+    const int from = path[i];
+    if (from != i) {
+      const __half* src = kv_k_ptr(g, lane, slot, pos0 + from, h, status);
+      __half* dst = kv_k_ptr(g, lane, slot, pos0 + i, h, status);
+      if (src && dst)
+        for (int e = threadIdx.x; e < g.hd; e += blockDim.x) {
+          dst[e] = src[e];
+          dst[v_off + e] = src[v_off + e];
+        }
+    }
+    __syncthreads();
+  }
+}
+
 // Lanes of a decode call: set the request and token budget.  A request above
 // the lane's cap sets ST_EKV and leaves the lane out.
 __global__ void decode_init_kernel(LaneState* __restrict__ lanes, int n_lanes, const int32_t* __restrict__ req_L,

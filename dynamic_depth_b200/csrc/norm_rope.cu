@@ -8,6 +8,7 @@
 // once, in the order of the projection row, so the pass is bound by memory.
 #include "common.cuh"
 #include "host_util.h"
+#include "tree_attn.h"
 
 namespace tl {
 namespace norm_rope {
@@ -29,6 +30,9 @@ struct Args {
   int32_t shift;
   void* q;
   int32_t* status;
+  // a context's lane: slots count positions of one cache slot of the lane, whose pages are map[0 .. map_pages)
+  const int32_t* map;
+  int32_t map_pages;
 };
 
 template <class T>
@@ -132,7 +136,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   if (is_q) {
     dst = static_cast<TC*>(a.q) + (row * a.H + h) * HD;
   } else {
-    const int64_t slot = a.slots[row];
+    int64_t slot = a.slots[row];
+    if (a.map && slot >= 0) {
+      const int64_t i = slot >> a.shift;
+      const int page = i < a.map_pages ? a.map[i] : -1;
+      slot = page < 0 ? -2 : ((int64_t)page << a.shift) + (slot & ((1 << a.shift) - 1));
+    }
     if (slot < 0 || slot >= a.n_slots) {
       if (slot != -1 && part == 0 && a.status) atomicOr(a.status, TL_BAD_SLOT);
       return;
@@ -176,6 +185,16 @@ static int launch_in(const Args& a, int dtype, int hd, cudaStream_t s) {
 }
 
 }  // namespace norm_rope
+
+int norm_rope_lane(const float* qkv, int64_t rows, int32_t n_heads, const float2* table, int32_t length,
+                   const int32_t* positions, const int64_t* slots, const tl_kv_pool& pool, const int32_t* map,
+                   int32_t map_pages, __half* q_out, int32_t* status, cudaStream_t s) {
+  norm_rope::Args a{qkv, rows, 3 * (int64_t)n_heads * pool.head_dim, n_heads, n_heads, nullptr, nullptr, 0.f, table,
+                    length, positions, slots, pool.dev_pool, pool.n_pages * pool.page_tokens, 0, q_out, status, map,
+                    map_pages};
+  while ((1 << a.shift) < pool.page_tokens) ++a.shift;
+  return norm_rope::launch<float, __half>(a, pool.head_dim, s);
+}
 
 // The pool of the serving operators: sizes, alignment, and rows within a tensor map's 32-bit coordinates.
 bool kv_pool_ok(const tl_kv_pool* p) {
@@ -222,7 +241,7 @@ extern "C" int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t r
     return TL_EINVAL;
   norm_rope::Args a{dev_qkv, rows, row_stride, n_heads, pool->n_kv_heads, dev_q_gain, dev_k_gain, eps,
                     reinterpret_cast<const float2*>(dev_table), length, dev_positions, dev_slots, pool->dev_pool,
-                    pool->n_pages * pool->page_tokens, 0, dev_q_out, dev_status};
+                    pool->n_pages * pool->page_tokens, 0, dev_q_out, dev_status, nullptr, 0};
   while ((1 << a.shift) < pool->page_tokens) ++a.shift;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   return pool->dtype == TL_F16 ? norm_rope::launch_in<__half>(a, dtype, pool->head_dim, s)

@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "tree_attn.h"
 #include "attn_decode.cuh"
 #include "attn_split.cuh"
 #include "attn_tc.cuh"
@@ -203,11 +204,18 @@ static GsChoice gs_plan(int fmt, int N, int K, int group, int nmat, int n_sms, i
   return c;
 }
 
+// Nodes of a draft tree, and the words of its tables (see TreeTab).
+static constexpr int kMaxTreeNodes = 256, kTreeMaskWords = kMaxTreeNodes / 32;
+static constexpr int kTreeInts = 32 + kMaxTreeNodes * (2 + 1 + 1 + 1 + 1 + kTreeMaskWords);
+static constexpr int kTreeSms = 148;  // SMs that the tree attention of a context uses, at most
+
 // Offsets of every workspace region (computed identically by tl_workspace_bytes and tl_create).
 struct Layout {
   int n_slots, pages_per_seq, n_pages, max_rows, n_parts, max_prefill;
   size_t page_elems;
   std::vector<size_t> mat_off;  // per matrix
+  int max_nodes;                // of a tl_speculate_tree call
+  size_t tree_tab, tree_ws;     // its tables, and the attention's workspace
   size_t gains, rope, page_table, kv, lanes, h, h_in, hrows, rows[6], act_a, act_qkv, act_q, act_o, act_u,
       act_a16, act_o16, act_u16, attn_part, attn_counters, part_val, part_idx, tok_stage, L_stage,
       mask_stage, pf_n, pf_tiles, pf_info, probe_logits, margin_lane, spec, lane_shared, casc,
@@ -293,6 +301,10 @@ static Layout make_layout(const tl_config* c) {
   L.b_part_val = take(lanes * L.n_parts * 4);
   L.b_part_idx = take(lanes * L.n_parts * 4);
   L.b_casc = take(lanes * c->n_heads * (hd + 2) * 4);
+  // tree speculation: node tables (kTreeInts words), an identity page table, and the attention's pieces
+  L.max_nodes = (int)std::min<size_t>(kMaxTreeNodes, std::min<size_t>(lanes, L.max_prefill));
+  L.tree_tab = take((size_t)(kTreeInts + 2 * L.pages_per_seq) * 4);
+  L.tree_ws = take(tree_attn_workspace(hd, L.max_nodes, kTreeSms));
   L.total = o;
   return L;
 }
@@ -857,6 +869,80 @@ int attn_prefill_launch(tl_ctx* c, int max_rows, const Rows& rows, int slot, con
   return prof_stop(c, TL_PROF_ATTN);
 }
 
+// Device tables of a draft tree (tl_speculate_tree), in c->tree_tab.
+struct TreeTab {
+  int32_t *cached, *fresh, *free_head, *ctx, *cu2;  // 1, 1, 1, 1, 2: inputs of the plan, and of one pass's attention
+  int32_t *cu, *lens, *granted, *head_out;          // 2, 1, 1, 1: the plan's small outputs
+  int64_t* slots;                                   // [nodes] positions of the nodes' keys
+  int32_t *tokens, *parents, *positions, *path;     // [nodes]
+  uint32_t* masks;                                  // [nodes][kTreeMaskWords]
+  int32_t *ident, *table;                           // [pages] 0, 1, 2, ..., and the plan's block table
+};
+TreeTab tree_tab(tl_ctx* c) {
+  int32_t* p = reinterpret_cast<int32_t*>(c->ws + c->lay.tree_tab);
+  TreeTab t;
+  t.cached = p;
+  t.fresh = p + 1;
+  t.free_head = p + 2;
+  t.ctx = p + 3;
+  t.cu2 = p + 4;
+  t.cu = p + 6;
+  t.lens = p + 8;
+  t.granted = p + 9;
+  t.head_out = p + 10;
+  p += 32;
+  t.slots = reinterpret_cast<int64_t*>(p);
+  t.tokens = p + 2 * kMaxTreeNodes;
+  t.parents = t.tokens + kMaxTreeNodes;
+  t.positions = t.parents + kMaxTreeNodes;
+  t.path = t.positions + kMaxTreeNodes;
+  t.masks = reinterpret_cast<uint32_t*>(t.path + kMaxTreeNodes);
+  t.ident = t.path + kMaxTreeNodes * (1 + kTreeMaskWords);
+  t.table = t.ident + c->lay.pages_per_seq;
+  return t;
+}
+
+// One pass over nodes node0 .. node0 + rows - 1 of a lane's tree.
+struct TreePass {
+  int lane, node0;
+  TreeTab tab;
+};
+
+// Rotation, append and attention of a tree pass's rows in one cache slot: the
+// operators of the serving calls on the lane's own pages.
+int tree_attn_launch(tl_ctx* c, const TreePass& t, int rows, int slot) {
+  TL_TRY(prof_start(c, TL_PROF_ATTN));
+  const tl_kv_pool pool{c->kv.pool, c->kv.n_pages, TL_F16, c->kv.H, c->hd, c->kv.page_tokens};
+  const int32_t* pages = c->page_table + ((int64_t)t.lane * c->lay.n_slots + slot) * c->lay.pages_per_seq;
+  __half* q16 = reinterpret_cast<__half*>(c->sc->act_q);
+  TL_TRY(norm_rope_lane(c->sc->act_qkv, rows, c->kv.H, c->rope, c->cfg.max_seq, t.tab.positions + t.node0,
+                        t.tab.slots + t.node0, pool, pages, c->lay.pages_per_seq, q16, c->status, c->stream));
+  c->launches++;
+  TreeAttnArgs a{};
+  a.q = q16;
+  a.q_stride = a.out_stride = c->cfg.d;
+  a.table = pages;
+  a.max_pages = c->lay.pages_per_seq;
+  a.ctx = t.tab.ctx;
+  a.cu = t.tab.cu2;
+  a.R = 1;
+  a.n_rows = a.max_nodes = rows;
+  a.H = c->kv.H;
+  a.masks = t.tab.masks + (size_t)t.node0 * kTreeMaskWords;
+  a.words = kTreeMaskWords;
+  a.node0 = t.node0;
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)c->hd);
+  a.out = c->sc->act_o;
+  a.out_f32 = 1;
+  a.out16 = c->sc->act_o16;
+  a.split16 = c->split16;
+  a.ws = c->ws + c->lay.tree_ws;
+  a.max_sms = kTreeSms;
+  a.status = c->status;
+  TL_TRY(tree_attn_run(a, pool, c->stream, &c->launches));
+  return prof_stop(c, TL_PROF_ATTN);
+}
+
 // Whether the few-row GEMV for W (nmat matrices) applies the RMSNorm in its
 // own activation staging (the streamed GEMV does; its fallback does not).
 bool gemv_norms_itself(tl_ctx* c, const MatView& W, int nmat) {
@@ -904,7 +990,8 @@ int norm_for_proj(tl_ctx* c, int max_rows, int path, const int32_t* n, float* hb
 // caller after the last block, from *pend).
 int run_block(tl_ctx* c, const Rows& rows, int max_rows, float* hbuf, const int32_t* map, const BlockW& w,
               int slot_base, int slot_stride, float* h_in, bool prompt = false, int path = PATH_AUTO,
-              const int2* tiles = nullptr, int n_tiles = 0, PendingAdd* pend = nullptr) {
+              const int2* tiles = nullptr, int n_tiles = 0, PendingAdd* pend = nullptr,
+              const TreePass* tree = nullptr) {
   if (prompt) path = max_rows > kGemvMaxRows ? PATH_TC : PATH_GEMV;
   const int d = c->cfg.d, F = c->cfg.ffn;
   const bool defer = pend && prompt && max_rows >= kWideRows;
@@ -926,7 +1013,9 @@ int run_block(tl_ctx* c, const Rows& rows, int max_rows, float* hbuf, const int3
   o.ldo = 3 * d;
   TL_TRY(proj(c, max_rows, path, X, 0, rows.n, pw.wqkv, &pw.mqkv, nullptr, nullptr, o, nullptr, TL_PROF_PROJ,
               use_nrm ? &nrm : nullptr, tb ? &t_qkv : nullptr));
-  if (prompt) {
+  if (tree) {
+    TL_TRY(tree_attn_launch(c, *tree, max_rows, slot_base));
+  } else if (prompt) {
     TL_TRY(launch_k(c, rope_kv_kernel, dim3(max_rows), dim3(d / 2), 0, c->sc->act_qkv, c->sc->act_q, rows, c->kv, c->rope,
                     slot_base, slot_stride, nullptr, c->status));
     TL_TRY(attn_prefill_launch(c, max_rows, rows, slot_base, tiles, n_tiles));
@@ -1776,19 +1865,22 @@ static int rerun_positions(tl_ctx* c, int lane, int pos0, int k, int L) {
   return TL_OK;
 }
 
-// Greedy head over hidden rows 0 .. k - 1 of c->hrows: dev_argmax[r] for each row.
-static int head_hrows(tl_ctx* c, int k, int32_t* dev_argmax) {
+// Head over hidden rows row0 .. row0 + k - 1 of c->hrows (k <= max_lanes): logits
+// [k][vocab] and dev_argmax[r] for each row (either may be null).
+static int head_hrows(tl_ctx* c, int k, int32_t* dev_argmax, float* logits = nullptr, int row0 = 0) {
   const Rows& T4 = c->rows[4];
   std::vector<int32_t> ident(k);
   for (int i = 0; i < k; ++i) ident[i] = i;
   TL_CUDA(cudaMemcpyAsync(T4.lane, ident.data(), k * 4, cudaMemcpyHostToDevice, c->stream));
   TL_CUDA(cudaMemcpyAsync(T4.n, &k, 4, cudaMemcpyHostToDevice, c->stream));
+  float* h = c->hrows + (size_t)row0 * c->cfg.d;
   const float* X = nullptr;
   GsNorm nrm{};
   bool use_nrm = false;
-  TL_TRY(norm_for_proj(c, k, PATH_AUTO, T4.n, c->hrows, nullptr, c->g_final, nullptr, c->head, 1, &X, &nrm, &use_nrm));
+  TL_TRY(norm_for_proj(c, k, PATH_AUTO, T4.n, h, nullptr, c->g_final, nullptr, c->head, 1, &X, &nrm, &use_nrm));
   ProjOut o{};
   o.epi = EPI_ARGMAX;
+  o.logits = logits;
   o.lmap = T4.lane;
   o.ldo = c->cfg.vocab;
   o.part_val = c->sc->part_val;
@@ -1796,6 +1888,7 @@ static int head_hrows(tl_ctx* c, int k, int32_t* dev_argmax) {
   o.n_parts_dev = c->sc->head_nparts;
   TL_TRY(proj(c, k, PATH_AUTO, X, 0, T4.n, c->head, &c->mhead, nullptr, nullptr, o, nullptr, TL_PROF_HEAD,
               use_nrm ? &nrm : nullptr));
+  if (!dev_argmax) return TL_OK;
   return launch_k(c, head_finalize_kernel, dim3(k), dim3(256), 0, T4, c->lanes, (const float*)c->sc->part_val,
                   (const int32_t*)c->sc->part_idx, (const int32_t*)c->sc->head_nparts, (int32_t)HEAD_ONLY, dev_argmax,
                   (int32_t*)nullptr, (int32_t*)nullptr, 0, c->embed, c->h, c->cfg.d, c->cfg.max_seq, 0, c->status,
@@ -1892,6 +1985,186 @@ extern "C" int tl_speculate(tl_ctx* c, int32_t lane, int32_t n_new, int32_t L_dr
   c->ee = ee;
   c->warm = wp;
   return st;
+}
+
+// ------------------------------------------------ speculation with a tree ----
+
+// Nodes lo .. hi - 1 of the lane's tree (tokens and tables on the device) through
+// embed, the pre blocks and L loop iterations; hidden rows in c->hrows[0 .. hi - lo).
+static int tree_pass(tl_ctx* c, const TreeTab& tab, int lane, int lo, int hi, int L) {
+  const tl_config& cfg = c->cfg;
+  const int P = cfg.n_pre, Lb = cfg.n_loop_layers, n = hi - lo;
+  const int32_t cu2[2] = {0, n};
+  TL_CUDA(cudaMemcpyAsync(tab.cu2, cu2, 8, cudaMemcpyHostToDevice, c->stream));
+  TL_CUDA(cudaMemcpyAsync(c->pf_n, &n, 4, cudaMemcpyHostToDevice, c->stream));
+  Rows Rs = c->rows[3];
+  Rs.n = c->pf_n;
+  const TreePass t{lane, lo, tab};
+  TL_TRY(launch_k(c, embed_rows_kernel, dim3(n), dim3(256), 0, c->embed, (const int32_t*)(tab.tokens + lo), n, cfg.d,
+                  c->hrows, c->status));
+  for (int b = 0; b < P; ++b)
+    TL_TRY(run_block(c, Rs, n, c->hrows, nullptr, c->pre[b], b, 0, nullptr, true, PATH_AUTO, nullptr, 0, nullptr, &t));
+  for (int l = 0; l < L; ++l)
+    for (int m = 0; m < Lb; ++m)
+      TL_TRY(run_block(c, Rs, n, c->hrows, nullptr, c->loop[m], P + l * Lb + m, 0, nullptr, true, PATH_AUTO, nullptr, 0,
+                       nullptr, &t));
+  c->prefill_tokens += n;
+  return TL_OK;
+}
+
+static int speculate_tree_impl(tl_ctx* c, int lane, int n_new, int Ld, int Lv, const int32_t* widths, int n_levels,
+                               int32_t* out, int32_t* rounds_out) {
+  const tl_config& cfg = c->cfg;
+  LaneState st{};
+  TL_CUDA(cudaMemcpyAsync(&st, c->lanes + lane, sizeof(st), cudaMemcpyDeviceToHost, c->stream));
+  TL_CUDA(cudaStreamSynchronize(c->stream));
+  if (st.phase != PH_BOUNDARY || st.taken != 0 || st.depth < Lv) return TL_ESTATE;
+  // level i holds nodes first[i] .. first[i + 1) - 1; level 0 is the last token taken
+  std::vector<int> first{0, 1};
+  for (int i = 0; i < n_levels; ++i) first.push_back(first[i + 1] + (first[i + 1] - first[i]) * widths[i]);
+  const int nodes = first[n_levels + 1], T = st.pos + 1;
+  if ((int64_t)T + n_new + nodes - 2 > cfg.max_seq) return TL_EINVAL;
+  std::vector<int32_t> parents(nodes, -1), ident(c->lay.pages_per_seq);
+  for (int i = 0; i < n_levels; ++i)
+    for (int j = first[i + 1]; j < first[i + 2]; ++j) parents[j] = first[i] + (j - first[i + 1]) / widths[i];
+  for (int i = 0; i < c->lay.pages_per_seq; ++i) ident[i] = i;
+  const TreeTab tab = tree_tab(c);
+  TL_CUDA(cudaMemcpyAsync(tab.parents, parents.data(), (size_t)nodes * 4, cudaMemcpyHostToDevice, c->stream));
+  TL_CUDA(cudaMemcpyAsync(tab.ident, ident.data(), ident.size() * 4, cudaMemcpyHostToDevice, c->stream));
+  TL_CUDA(cudaMemcpyAsync(tab.table, ident.data(), ident.size() * 4, cudaMemcpyHostToDevice, c->stream));
+  // token 0 from the prompt's last position
+  int32_t* tok = c->spec;
+  std::vector<uint8_t> mask(cfg.max_lanes, 0);
+  mask[lane] = 1;
+  TL_CUDA(cudaMemcpyAsync(c->mask_stage, mask.data(), cfg.max_lanes, cudaMemcpyHostToDevice, c->stream));
+  TL_TRY(build_rows(c, 1, SEL_MASK, c->mask_stage, nullptr, nullptr, nullptr));
+  TL_TRY(head_stage(c, cfg.max_lanes, HEAD_ONLY, nullptr, tok, nullptr, nullptr, 0));
+  int32_t t0 = 0;
+  TL_CUDA(cudaMemcpyAsync(&t0, tok + lane, 4, cudaMemcpyDeviceToHost, c->stream));
+  TL_CUDA(cudaStreamSynchronize(c->stream));
+  std::vector<int32_t> tokens{t0}, h_tok(nodes), h_pick(nodes), path;
+  int32_t* pick = c->spec + cfg.max_lanes;  // [nodes] the verify pass's greedy tokens
+  int rounds = 0;
+  while ((int)tokens.size() < n_new) {
+    ++rounds;
+    const int32_t p0 = T + (int)tokens.size() - 1;  // position of the last token taken, not computed yet
+    const int levels = std::min(n_levels, n_new - (int)tokens.size() - 1);
+    const int n = first[levels + 1];
+    // positions, masks and key slots of the nodes: the plan of one request on an identity page table
+    const int32_t in[4] = {p0, n, (p0 + cfg.kv_page_tokens - 1) / cfg.kv_page_tokens, p0};
+    TL_CUDA(cudaMemcpyAsync(tab.cached, in, sizeof(in), cudaMemcpyHostToDevice, c->stream));
+    TL_CUDA(cudaMemcpyAsync(tab.tokens, &tokens.back(), 4, cudaMemcpyHostToDevice, c->stream));
+    TL_TRY(tl_plan_batch(tab.cached, tab.fresh, 1, cfg.kv_page_tokens, tab.table, c->lay.pages_per_seq, tab.ident,
+                         c->lay.pages_per_seq, tab.free_head, tab.parents, n, kTreeMaskWords, tab.cu, tab.lens,
+                         tab.granted, tab.head_out, tab.slots, tab.positions, tab.masks, c->status, c->stream));
+    c->launches++;
+    // draft: a level at a time at L_draft, the best tokens of each node become its children
+    for (int i = 0; i < levels; ++i) {
+      const int lo = first[i], hi = first[i + 1];
+      TL_TRY(tree_pass(c, tab, lane, lo, hi, Ld));
+      TL_TRY(head_hrows(c, hi - lo, nullptr, c->probe_logits));
+      TL_TRY(tl_token_logprobs(c->probe_logits, TL_F32, hi - lo, cfg.vocab, cfg.vocab, nullptr, widths[i], nullptr,
+                               nullptr, nullptr, nullptr, tab.tokens + hi, nullptr, c->stream));
+      c->launches++;
+    }
+    // verify: the whole tree at L_verify
+    TL_TRY(tree_pass(c, tab, lane, 0, n, Lv));
+    TL_TRY(head_hrows(c, n, pick));
+    TL_CUDA(cudaMemcpyAsync(h_tok.data(), tab.tokens, (size_t)n * 4, cudaMemcpyDeviceToHost, c->stream));
+    TL_CUDA(cudaMemcpyAsync(h_pick.data(), pick, (size_t)n * 4, cudaMemcpyDeviceToHost, c->stream));
+    TL_CUDA(cudaStreamSynchronize(c->stream));
+    // keep the path along which each greedy choice was drafted
+    path.assign(1, 0);
+    tokens.push_back(h_pick[0]);
+    for (int i = 0; i < levels; ++i) {
+      const int w = widths[i], child0 = first[i + 1] + (path.back() - first[i]) * w;
+      int next = -1;
+      for (int j = child0; j < child0 + w; ++j)
+        if (h_tok[j] == tokens.back()) { next = j; break; }
+      if (next < 0) break;
+      path.push_back(next);
+      tokens.push_back(h_pick[next]);
+    }
+    const int kept = (int)path.size();
+    if (kept > 1) {  // their keys and values to consecutive positions
+      TL_CUDA(cudaMemcpyAsync(tab.path, path.data(), (size_t)kept * 4, cudaMemcpyHostToDevice, c->stream));
+      TL_TRY(launch_k(c, tree_path_kernel, dim3(cfg.n_pre + Lv * cfg.n_loop_layers, cfg.n_heads), dim3(32), 0, c->kv,
+                      lane, (int)p0, (const int32_t*)tab.path, kept, c->status));
+    }
+    // the lane continues from the last kept position, computed at L_verify by the verify pass
+    const int32_t info[4] = {lane, path.back(), p0 + kept - 1, Lv};
+    TL_CUDA(cudaMemcpyAsync(c->pf_info, info, sizeof(info), cudaMemcpyHostToDevice, c->stream));
+    TL_TRY(launch_k(c, prefill_finish_batch_kernel, dim3(1), dim3(256), 0, c->lanes, (const int32_t*)c->pf_info, 1,
+                    (const float*)c->hrows, c->h, cfg.d));
+  }
+  TL_CUDA(cudaStreamSynchronize(c->stream));
+  std::memcpy(out, tokens.data(), (size_t)n_new * 4);
+  if (rounds_out) *rounds_out = rounds;
+  return TL_OK;
+}
+
+extern "C" int tl_speculate_tree(tl_ctx* c, int32_t lane, int32_t n_new, int32_t L_draft, int32_t L_verify,
+                                 const int32_t* host_widths, int32_t n_levels, int32_t* host_tokens_out,
+                                 int32_t* host_rounds_out) {
+  if (!c || !host_widths || !host_tokens_out) return TL_EINVAL;
+  if (!c->loaded) return TL_ESTATE;
+  if (lane < 0 || lane >= c->cfg.max_lanes || c->cfg.vocab > (1 << 20) || n_new < 1 || L_draft < 1 ||
+      L_draft > L_verify ||
+      L_verify > c->cfg.L_max || n_levels < 1 || n_levels > kMaxTreeNodes)
+    return TL_EINVAL;
+  int64_t level = 1, nodes = 1;
+  for (int i = 0; i < n_levels; ++i) {
+    if (host_widths[i] < 1 || host_widths[i] > 64 || host_widths[i] > c->cfg.vocab) return TL_EINVAL;
+    level *= host_widths[i];
+    nodes += level;
+    if (nodes > c->lay.max_nodes) return TL_EINVAL;
+  }
+  if (c->lane_L[lane] == 0) return TL_ESTATE;
+  if (L_verify > c->lane_L[lane]) return TL_EKV;
+  try {
+    return speculate_tree_impl(c, lane, n_new, L_draft, L_verify, host_widths, n_levels, host_tokens_out,
+                               host_rounds_out);
+  } catch (const std::bad_alloc&) {
+    return TL_ENOMEM;
+  }
+}
+
+// ---------------------------------------------------------------- scoring ----
+
+extern "C" int tl_score(tl_ctx* c, int32_t lane, const int32_t* host_tokens, int32_t T, int32_t L, int32_t share_from,
+                        int32_t shared_tokens, int32_t n_top, float* dev_logprob, int32_t* dev_rank,
+                        float* dev_entropy, float* dev_lse, int32_t* dev_top_ids, float* dev_top_logprobs,
+                        int32_t* host_rows_out) {
+  if (!c || !host_tokens || c->cfg.vocab > (1 << 20) || n_top < 0 || n_top > 64 || n_top > c->cfg.vocab ||
+      ((dev_top_ids || dev_top_logprobs) && n_top == 0))
+    return TL_EINVAL;
+  const void* outs[] = {dev_logprob, dev_rank, dev_entropy, dev_lse, dev_top_ids, dev_top_logprobs};
+  for (const void* p : outs)
+    if ((uintptr_t)p & 3) return TL_EINVAL;
+  if (!c->loaded) return TL_ESTATE;
+  try {
+    TL_TRY(prefill_impl(c, {PromptLane{lane, host_tokens, T, L}}, share_from, shared_tokens, nullptr));
+    const int pos0 = c->h_lane_shared[lane], rows = T - pos0;
+    if (host_rows_out) *host_rows_out = rows;
+    // the target of a position is the token behind it; the last has none
+    std::vector<int32_t> next(host_tokens + pos0 + 1, host_tokens + T);
+    next.push_back(-1);
+    int32_t* targets = c->spec + c->cfg.max_lanes;
+    TL_CUDA(cudaMemcpyAsync(targets, next.data(), (size_t)rows * 4, cudaMemcpyHostToDevice, c->stream));
+    for (int r0 = 0; r0 < rows; r0 += c->cfg.max_lanes) {
+      const int n = std::min(c->cfg.max_lanes, rows - r0);
+      TL_TRY(head_hrows(c, n, nullptr, c->probe_logits, r0));
+      TL_TRY(tl_token_logprobs(c->probe_logits, TL_F32, n, c->cfg.vocab, c->cfg.vocab, targets + r0, n_top,
+                               dev_logprob ? dev_logprob + r0 : nullptr, dev_rank ? dev_rank + r0 : nullptr,
+                               dev_entropy ? dev_entropy + r0 : nullptr, dev_lse ? dev_lse + r0 : nullptr,
+                               dev_top_ids ? dev_top_ids + (size_t)r0 * n_top : nullptr,
+                               dev_top_logprobs ? dev_top_logprobs + (size_t)r0 * n_top : nullptr, c->stream));
+      c->launches++;
+    }
+    return TL_OK;
+  } catch (const std::bad_alloc&) {
+    return TL_ENOMEM;
+  }
 }
 
 extern "C" int tl_loop_step(tl_ctx* c, const int32_t* dev_L, const uint8_t* dev_mask, uint8_t* dev_exit) {

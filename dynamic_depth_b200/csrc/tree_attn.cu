@@ -140,11 +140,12 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r) {
   Req q;
   const int c0 = a.cu[r], c1 = a.cu[r + 1], ctx = a.ctx[r];
   const int64_t cap = (int64_t)a.max_pages << a.page_shift;
-  q.bad = c0 < 0 || c1 < c0 || c1 > a.n_rows || c1 - c0 > a.max_nodes || ctx < 0 || (int64_t)ctx + (c1 - c0) > cap;
+  q.bad = c0 < 0 || c1 < c0 || c1 > a.n_rows || c1 - c0 > a.max_nodes || ctx < 0 ||
+          (int64_t)ctx + a.node0 + (c1 - c0) > cap;
   q.row0 = c0;
   q.n = q.bad ? 0 : c1 - c0;
   q.ctx = ctx;
-  q.len = ctx + q.n;
+  q.len = ctx + a.node0 + q.n;
   q.tiles = q.len > 0 ? (q.len + KT - 1) / KT : 1;
   q.blocks = (int)(((int64_t)q.n * (a.H / a.Hk) + BM - 1) / BM);
   return q;
@@ -420,12 +421,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
                   const int nd = node[e >> 1];
                   see = nd >= 0 && (a.masks ? j < 32 * a.words &&
                                                   (__ldg(a.masks + row[e >> 1] * a.words + (j >> 5)) >> (j & 31) & 1u)
-                                            : j <= nd);
+                                            : j <= nd + a.node0);
                 }
                 if (!see) S[i][e] = -INFINITY;
               }
             // values of positions that nobody sees may be anything: 0 * NaN is not 0
-            const bool scan = q.n > 1 || a.masks;
+            const bool scan = q.len > q.ctx + 1 || a.masks;
             for (int i = lane; i < KW * (HD / 8); i += 32) {
               const int y = wn * KW + i / (HD / 8), pos = t * KT + y;
               uint4* p = reinterpret_cast<uint4*>(sv + (at(va, y, i % (HD / 8)) - va));
@@ -741,6 +742,7 @@ size_t tree_attn_workspace(int hd, int64_t rows_per_head, int n_sms) {
 int tree_attn_run(TreeAttnArgs a, const tl_kv_pool& p, cudaStream_t s, int64_t* launches) {
   int n_sms = 0;
   TL_TRY(tree::sm_count(&n_sms));
+  if (a.max_sms && n_sms > a.max_sms) n_sms = a.max_sms;
   a.Hk = p.n_kv_heads;
   a.n_pages = p.n_pages;
   a.page_shift = 0;

@@ -191,7 +191,7 @@ __device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q
       auto word = [&](int i) { return i >= 0 && i < a.words ? __ldg(w + i) : 0u; };
       v |= j0 >= 0 ? __funnelshift_r(word(j0 >> 5), word((j0 >> 5) + 1), j0 & 31) : word(0) << -j0;
     } else {
-      v |= low(node + 1 - j0) & ~low(-j0);
+      v |= low(node + a.node0 + 1 - j0) & ~low(-j0);
     }
   }
   return v & low(q.len - p0);
@@ -464,7 +464,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
             if (pos >= len || !(landed >> (y / PR) & 1u)) {
 #pragma unroll
               for (int c = 0; c < HD / 16; ++c) *chunk(c0 + c) = make_uint4(0, 0, 0, 0);
-            } else if (pos >= ctx && (s.q.n > 1 || a.masks)) {
+            } else if (pos >= ctx && (len > ctx + 1 || a.masks)) {
 #pragma unroll
               for (int c = 0; c < HD / 16; ++c) {
                 const uint4 w = *chunk(c0 + c);

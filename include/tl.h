@@ -346,6 +346,39 @@ int tl_generate(tl_ctx* ctx, const int32_t* host_prompts, int32_t n_lanes, int32
 int tl_speculate(tl_ctx* ctx, int32_t lane, int32_t n_new, int32_t L_draft, int32_t L_verify, int32_t draft_ahead,
                  int32_t* host_tokens_out, int32_t* host_rounds_out);
 
+/* tl_speculate with a tree of drafts.  A round drafts level by level at
+ * L_draft: the last token taken is the root, and every node of level i gets
+ * the host_widths[i] best tokens of its head as children (in the order of
+ * tl_token_logprobs); then all nodes run at L_verify in one pass, each seeing
+ * the cache, its ancestors and itself, and the path from the root along which
+ * every greedy choice of the verify pass was drafted is kept, with one more
+ * token, the choice at its end.  The kept nodes' K/V move to consecutive
+ * positions.  Widths of 1 draft a chain.  The tokens are those of a plain
+ * decode at L_verify; the tree only decides how many positions a round covers:
+ * up to n_levels + 1 tokens.
+ *   host_widths: int32 [n_levels], each 1 .. 64; the tree's nodes, 1 + w0 +
+ *     w0 w1 + ..., at most 256, max_lanes and max_prefill_tokens.  Rounds near
+ *     the end draft fewer levels.
+ *   1 <= L_draft <= L_verify; prompt length + n_new + nodes - 2 <= max_seq
+ *     (draft positions are cached behind the lane's).
+ * The lane's condition before and after, and the other arguments and errors,
+ * are tl_speculate's; vocab <= 2^20 (TL_EINVAL). */
+int tl_speculate_tree(tl_ctx* ctx, int32_t lane, int32_t n_new, int32_t L_draft, int32_t L_verify,
+                      const int32_t* host_widths, int32_t n_levels, int32_t* host_tokens_out,
+                      int32_t* host_rounds_out);
+
+/* Score a prompt ("CLI Reference", "benchmark": forward scoring over a token
+ * sequence at --loops L): tl_prefill, then the head over every position
+ * computed (all T without a shared prefix), max_lanes positions at a time, and
+ * tl_token_logprobs with each position's next token as its target (the last
+ * position has none: logprob 0, rank -1).  Arguments and effect on the lane as
+ * tl_prefill; outputs as tl_token_logprobs, one row per position computed, any
+ * of them NULL.  host_rows_out: NULL or the number of rows.  vocab <= 2^20. */
+int tl_score(tl_ctx* ctx, int32_t lane, const int32_t* host_tokens, int32_t T, int32_t L,
+             int32_t share_prefix_from_lane, int32_t shared_tokens, int32_t n_top, float* dev_logprob,
+             int32_t* dev_rank, float* dev_entropy, float* dev_lse, int32_t* dev_top_ids, float* dev_top_logprobs,
+             int32_t* host_rows_out);
+
 /* Layout of a decode tick ("Depth-adaptive Inference of Looped Language
  * Models via Continuous Depth Batching": boundary stages queued apart from
  * loop steps, with scheduling overlapping GPU work).  In modes 1 and 2 every
