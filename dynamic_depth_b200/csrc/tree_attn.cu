@@ -693,7 +693,13 @@ static int launch(K kern, int ctas, int threads, int smem, const TreeAttnArgs& a
   TL_TRY(encode_map_2d(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.dev_pool, HD,
                        rows, HD * 2, cols, p.page_tokens < KT ? p.page_tokens : KT,
                        cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
-  TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static uint64_t set = 0;  // per kernel: one bit per device
+  int dev = 0;
+  TL_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !(set >> dev & 1)) {
+    TL_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (dev < 64) set |= 1ull << dev;
+  }
   kern<<<ctas, threads, smem, s>>>(map, a);
   TL_CUDA(cudaGetLastError());
   cudaLaunchConfig_t lc{};

@@ -52,23 +52,45 @@ def _flat(t, dtype, n, name, device):
     return t.data_ptr()
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+# A call costs its wrapper before it costs the GPU anything: streams and outputs come from torch's raw entry points
+# where it has them (0.1 against 3.3 us for the current stream, 0.6 against 2.3 us for an empty tensor).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
+
 class _on:
-    """The device of a call made current, where it is not; .stream is its current stream."""
+    """The device of a call made current where it is not; entering gives its current stream."""
 
     def __init__(self, device):
         _need(device.type == "cuda", "the tensors must be on a CUDA device")
+        self.index = device.index if device.index is not None else torch.cuda.current_device()
         self.guard = None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        if self.guard:
+        if self.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         if self.guard:
             self.guard.__exit__(*exc)
+
+
+def _empty(dtype, *shape):
+    """A contiguous tensor of up to three dimensions on the current device."""
+    if _empty_strided_cuda is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    n = len(shape)
+    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
+    return _empty_strided_cuda(shape, strides, dtype)
 
 
 def _pool(pool) -> TlKvPool:
@@ -87,17 +109,17 @@ def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
     dev = logits.device
     tp = _flat(targets, torch.int32, rows, "targets", dev)
     with _on(dev) as stream:
-        f = torch.empty((3, rows), dtype=torch.float32, device=dev)
-        lp, ent, lse = f.unbind(0)
-        rank = torch.empty(rows, dtype=torch.int32, device=dev) if targets is not None else None
-        ids = torch.empty((rows, n_top), dtype=torch.int32, device=dev) if n_top else None
-        top = torch.empty((rows, n_top), dtype=torch.float32, device=dev) if n_top else None
+        f32, i32 = torch.float32, torch.int32
+        lp = rank = ids = top = None
+        if targets is not None:
+            lp, rank = _empty(f32, rows), _empty(i32, rows)
+        ent, lse = _empty(f32, rows), _empty(f32, rows)
+        if n_top:
+            ids, top = _empty(i32, rows, n_top), _empty(f32, rows, n_top)
         check(lib().tl_token_logprobs(
             logits.data_ptr(), _DT[logits.dtype], rows, vocab, logits.stride(0) if rows > 1 else vocab, tp, n_top,
-            lp.data_ptr() if tp is not None else None, rank.data_ptr() if rank is not None else None, ent.data_ptr(),
-            lse.data_ptr(), ids.data_ptr() if n_top else None, top.data_ptr() if n_top else None, stream),
-            "tl_token_logprobs")
-    return TokenLogprobs(lp if targets is not None else None, rank, ent, lse, ids, top)
+            _at(lp), _at(rank), ent.data_ptr(), lse.data_ptr(), _at(ids), _at(top), stream), "tl_token_logprobs")
+    return TokenLogprobs(lp, rank, ent, lse, ids, top)
 
 
 def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: int, n_rows: int, parents=None,
@@ -120,15 +142,12 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
     st = _flat(status, i32, 1, "status", dev)
     _need(0 <= mask_words <= 8 and n_rows >= 0, "mask_words 0 .. 8, n_rows >= 0")
     with _on(dev) as stream:
-        small = torch.empty(3 * R + 2, dtype=i32, device=dev)
-        cu, lens, granted, head = small[:R + 1], small[R + 1:2 * R + 1], small[2 * R + 1:3 * R + 1], small[3 * R + 1:]
-        slots = torch.empty(n_rows, dtype=torch.int64, device=dev)
-        pos = torch.empty(n_rows, dtype=i32, device=dev)
-        masks = torch.empty((n_rows, mask_words), dtype=i32, device=dev) if mask_words else None
-        at = small.data_ptr()
+        cu, lens, granted, head = _empty(i32, R + 1), _empty(i32, R), _empty(i32, R), _empty(i32, 1)
+        slots, pos = _empty(torch.int64, n_rows), _empty(i32, n_rows)
+        masks = _empty(i32, n_rows, mask_words) if mask_words else None
         # an empty tensor has no address; the library wants one where a mask is asked for
-        mp = None if masks is None else (masks.data_ptr() or at)
-        check(lib().tl_plan_batch(*args, at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (3 * R + 1),
+        mp = None if masks is None else (masks.data_ptr() or cu.data_ptr())
+        check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
                                   slots.data_ptr(), pos.data_ptr(), mp, st, stream), "tl_plan_batch")
     return BatchPlan(cu, lens, granted, head, slots, pos, masks)
 
@@ -137,7 +156,7 @@ def rope_table(length: int, head_dim: int, base: float = 1e4, device="cuda") -> 
     """(cos, sin) of position * base^(-2i / head_dim): fp32 [length, head_dim / 2, 2], angles in fp64."""
     dev = torch.device(device)
     with _on(dev) as stream:
-        t = torch.empty((length, head_dim // 2, 2), dtype=torch.float32, device=dev)
+        t = _empty(torch.float32, length, head_dim // 2, 2)
         check(lib().tl_rope_table(t.data_ptr(), length, head_dim, float(base), stream), "tl_rope_table")
     return t
 
@@ -159,7 +178,7 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
     st = _flat(status, i32, 1, "status", dev)
     with _on(dev) as stream:
         if q_out is None:
-            q_out = torch.empty((rows, n_heads, hd), dtype=pool.dtype, device=dev)
+            q_out = _empty(pool.dtype, rows, n_heads, hd)
         qp = _flat(q_out, pool.dtype, rows * n_heads * hd, "q_out", dev)
         check(lib().tl_norm_rope_append(qkv.data_ptr(), _DT[qkv.dtype], rows,
                                         qkv.stride(0) if rows > 1 else qkv.shape[1], n_heads, gq, gk, eps, rp,
@@ -174,7 +193,7 @@ def tree_attention_workspace(head_dim: int, n_heads: int, n_kv_heads: int, max_n
     with _on(dev):
         check(lib().tl_tree_attention_workspace(head_dim, n_heads, n_kv_heads, max_nodes, C.byref(n)),
               "tl_tree_attention_workspace")
-        return torch.empty(n.value, dtype=torch.uint8, device=dev)
+        return _empty(torch.uint8, n.value)
 
 
 def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=None, scale: float = 0.0, out=None,
@@ -201,18 +220,18 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     st = _flat(status, i32, 1, "status", dev)
     with _on(dev) as stream:
         if out is None:
-            out = torch.empty((rows, H, hd), dtype=q.dtype, device=dev)
+            out = _empty(q.dtype, rows, H, hd)
         _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1 and out.stride(1) == hd
               and out.device == dev, "out: the shape of q, heads adjacent")
-        lse = torch.empty((rows, H), dtype=torch.float32, device=dev) if return_lse else None
+        lse = _empty(torch.float32, rows, H) if return_lse else None
         if workspace is None:
             n = C.c_size_t()
             check(lib().tl_tree_attention_workspace(hd, H, p.n_kv_heads, max_nodes, C.byref(n)),
                   "tl_tree_attention_workspace")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            workspace = _empty(torch.uint8, n.value)
         check(lib().tl_tree_attention(
             q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
             block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
-            out.stride(0) if rows > 1 else H * hd, lse.data_ptr() if return_lse else None, workspace.data_ptr(),
+            out.stride(0) if rows > 1 else H * hd, _at(lse), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), st, stream), "tl_tree_attention")
     return (out, lse) if return_lse else out
