@@ -1285,6 +1285,23 @@ int encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
   return encode_2d(m, dt, base, inner, outer, row_bytes, box_inner, box_outer, sw);
 }
+
+int encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                  const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw) {
+  auto fn = tensor_map_encoder();
+  if (!fn) {
+    g_cuda_err = "cuTensorMapEncodeTiled entry point unavailable";
+    return TL_ECUDA;
+  }
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
+  if (fn(m, dt, 4, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+    g_cuda_err = "cuTensorMapEncodeTiled failed";
+    return TL_ECUDA;
+  }
+  return TL_OK;
+}
 }  // namespace tl
 
 // ============================================================== C ABI ====

@@ -5,20 +5,23 @@
 // context and its own nodes, read from the pages by TMA in tiles of KT
 // positions.  Work is cut into units of one key tile of one (request, key
 // head, block of BM query rows); the units, in that order, are dealt in equal
-// contiguous ranges to one persistent CTA per SM, so ragged lengths and few
-// long requests fill the machine alike.  A CTA whose range covers all tiles of
+// contiguous ranges to two persistent CTAs per SM, so ragged lengths and few
+// long requests fill the machine alike, and one CTA streams while the other is
+// between row blocks.  A CTA whose range covers all tiles of
 // a row block writes the result; a block cut by range boundaries leaves
 // (max, sum, output) pieces in the workspace - at most two per CTA, whatever
 // the problem - and a second, small kernel joins them in order.  No atomics:
 // results do not depend on timing.
 //
 // Inside a CTA (flash attention, one pass over the keys with a running maximum
-// and sum per row): a producer warp loads tiles into a ring of stages; eight
-// warps multiply, in two groups of four that take alternate tiles, each group
-// split over BM / 16 row blocks and, where those are fewer than four, over
-// parts of the tile's keys.  Every warp keeps its own running state over the
-// keys it sees; the states of a row block meet once per block, in shared
-// memory.
+// and sum per row): a producer warp loads tiles into a ring of stages; four
+// warps multiply, split over the block's 16-row parts and, where those are
+// fewer than four, over parts of the tile's keys.  Every warp keeps its own
+// running state over the keys it sees; the states of a row block meet once per
+// block, in shared memory.  A page's part of a tile, keys and values of one
+// head, is one four-dimensional TMA box: with one box per 64 columns of keys or
+// values, pages of 16 positions streamed at 4.4 TB/s where pages of 64 reached
+// 5.6.
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.
@@ -36,10 +39,12 @@ namespace tl {
 // Driver entry point of the tensor-map encoder and 2D maps of row-major arrays (runtime.cu).
 int encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+int encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                  const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
 
 namespace tree {
 
-constexpr int kWarps = 8;                     // consumer warps
+constexpr int kWarps = 4;                     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -49,17 +54,12 @@ struct Cfg {
   static constexpr int COLS = HD < 64 ? HD : 64;    // columns of a TMA box (one swizzled row)
   static constexpr int CT = HD / COLS;
   static constexpr int ROWB = COLS * 2;             // bytes of a box row
-  static constexpr int TILE = KT * ROWB;
-  static constexpr int STAGE = 2 * CT * TILE;       // K boxes, then V boxes
-  // Even, so that a stage always belongs to the same group of warps: with an odd number, a group ahead of the
-  // other could wait for a stage's next round while this round's copy is still in flight, and a wait by parity
-  // takes the round before for it.
-  static constexpr int STAGES = HD == 32 ? 8 : 4;
+  static constexpr int STAGE = 2 * KT * HD * 2;     // K and V of a tile
+  static constexpr int STAGES = HD == 32 ? 4 : 2;
   static constexpr int SLOT = (HD / 2 + 4) * 32;    // floats of one warp's state: output, 2 maxima, 2 sums
-  static constexpr int MERGE = 4 * SLOT * 4;
+  static constexpr int MERGE = 2 * SLOT * 4;
   static constexpr int SMEM = 1024 + STAGES * STAGE + MERGE + 256;
-  static_assert(SMEM <= 227 * 1024, "tile ring does not fit");
-  static_assert(STAGES % 2 == 0, "a stage serves one group of warps");
+  static_assert(SMEM + 1024 <= 113 * 1024, "two CTAs per SM");
 };
 
 struct Req {
@@ -239,14 +239,14 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, Range* sh, lon
 }
 
 // The producer warp: the tiles of the CTA's range into the ring, a box per page
-// (or part of one), K and V of each.
+// (or part of one) with the keys and values of its positions: [K, V][column
+// tiles][positions][64 columns].
 template <class C, int KT, int BM>
 __device__ __forceinline__ void produce(const TreeAttnArgs& a, const CUtensorMap& kvmap, Walk<KT, BM> walk,
                                         uint8_t* ring, uint64_t* full, uint64_t* empty, volatile uint32_t* info,
                                         volatile int32_t* abort_flag) {
-  constexpr int ROWB = C::TILE / KT;
   const int lane = threadIdx.x & 31;
-  const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR;
+  const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR, box_bytes = C::STAGE / boxes;
   Seg s;
   int k = 0;
   bool ok = true;
@@ -269,17 +269,12 @@ __device__ __forceinline__ void produce(const TreeAttnArgs& a, const CUtensorMap
       const uint32_t bar = smem_u32(&full[st]);
       if (lane == 0) {
         info[st] = in;
-        mbar_expect_tx(bar, __popc(in) * 2 * C::CT * PR * ROWB);
+        mbar_expect_tx(bar, __popc(in) * box_bytes);
       }
       __syncwarp();
       if (good) {
         const int64_t y = (((int64_t)page * 2 * a.Hk + s.hk) << a.page_shift) + (pos & (P - 1));
-        const uint32_t dst = smem_u32(ring + st * C::STAGE) + lane * PR * ROWB;
-#pragma unroll
-        for (int ct = 0; ct < C::CT; ++ct) {
-          tma_load_2d(dst + ct * C::TILE, &kvmap, ct * 64, (int)y, bar);
-          tma_load_2d(dst + (C::CT + ct) * C::TILE, &kvmap, ct * 64, (int)(y + ((int64_t)a.Hk << a.page_shift)), bar);
-        }
+        tma_load_4d(smem_u32(ring + st * C::STAGE) + lane * box_bytes, &kvmap, 0, (int)y, 0, 0, bar);
       }
       __syncwarp();
       page = next_page;
@@ -301,14 +296,14 @@ namespace tl {
 namespace tree {
 
 template <int HD, int WM, bool BF>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a) {
   using C = Cfg<HD>;
   constexpr int KT = C::KT, BM = 16 * WM, WN = 4 / WM, KW = KT / WN, NT = KW / 8;
   extern __shared__ __align__(1024) uint8_t smem_ta[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_ta) + 1023) & ~uintptr_t(1023));
   float* merge = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(merge + 4 * C::SLOT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(merge + 2 * C::SLOT);
   uint64_t* empty = full + C::STAGES;
   volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(empty + C::STAGES);  // [STAGES] boxes that landed
   __shared__ int32_t abort_s;
@@ -340,10 +335,25 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
       produce<C, KT, BM>(a, kvmap, walk, ring, full, empty, info, abort_flag);
     } else {
       // ----------------------------------------------------------- consumers
-      const int grp = warp >> 2, wm = (warp & 3) % WM, wn = (warp & 3) / WM;
-      const int part = grp * WN + wn;  // of the 2 WN warps that share a row block
+      const int wm = warp % WM, wn = warp / WM;
+      // a 16-byte chunk of a tile row: the row's box, the head's K or V in it, the row, the chunk swizzled by the row
+      const int pshift = 31 - __clz(PR), box_bytes = C::STAGE / boxes, col_bytes = PR * C::ROWB;
+      auto row_at = [&](int y) { return (y >> pshift) * box_bytes + (y & (PR - 1)) * C::ROWB; };
+      auto chunk_at = [&](int y, int c) {  // c static or not; K (V: + CT column tiles)
+        const int sw = C::ROWB == 128 ? (y & 7) : ((y >> 1) & 3);
+        return row_at(y) + (c / (C::COLS / 8)) * col_bytes + (((c % (C::COLS / 8)) ^ sw) << 4);
+      };
       const int G = a.H / a.Hk;
       const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // the thread's rows r0, r0 + 8; columns c0, c0 + 1 of each 8
+      // the lane's rows of the 16-key steps that it addresses for ldmatrix, and its swizzled column bits
+      uint32_t k_row[NT / 2], v_row[NT / 2];
+      const int sw = C::ROWB == 128 ? (lane & 7) : ((lane & 7) >> 1);
+      const uint32_t k_col = (((lane >> 3) & 1) ^ sw) << 4, v_col = (((lane >> 4) & 1) ^ sw) << 4;
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        k_row[j] = row_at(wn * KW + j * 16 + (lane & 7) + ((lane >> 4) & 1) * 8);
+        v_row[j] = row_at(wn * KW + j * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
+      }
       bool ok = true;
       while (walk.next(a, s)) {
         const Req& q = s.q;
@@ -377,21 +387,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
 
         for (int t = s.t0; t < s.t1; ++t, ++k) {
-          if ((k & 1) != grp) continue;
           const int st = k % C::STAGES;
           if (ok) ok = mbar_wait_warp(smem_u32(&full[st]), (k / C::STAGES) & 1, abort_flag);
           if (!ok) continue;
           uint8_t* sk = ring + st * C::STAGE;
-          uint8_t* sv = sk + C::CT * C::TILE;
+          uint8_t* sv = sk + C::CT * col_bytes;
           const uint32_t ka = smem_u32(sk), va = smem_u32(sv);
           const uint32_t landed = info[st];
           const int key0 = t * KT + wn * KW;  // first position of this warp's part
-          // swizzled address of 16-byte column chunk c of tile row y
-          auto at = [&](uint32_t base, int y, int c) {
-            const int ct = c / (C::COLS / 8), cc = c % (C::COLS / 8);
-            const int sw = C::ROWB == 128 ? (y & 7) : ((y >> 1) & 3);
-            return base + ct * C::TILE + y * C::ROWB + ((cc ^ sw) << 4);
-          };
           // -------------------------------------------------- S = Q K^T
           float S[NT][4];
 #pragma unroll
@@ -403,7 +406,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) {
               uint32_t b[4];
-              ldsm4(at(ka, wn * KW + j * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, kk * 2 + ((lane >> 3) & 1)), b);
+              ldsm4(ka + k_row[j] + (kk * 2 / (C::COLS / 8)) * col_bytes + ((kk * 2 % (C::COLS / 8) * 16) ^ k_col), b);
               mma16816<BF>(S[2 * j], qf[kk], b[0], b[1]);
               mma16816<BF>(S[2 * j + 1], qf[kk], b[2], b[3]);
             }
@@ -429,7 +432,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
             const bool scan = q.len > q.ctx + 1 || a.masks;
             for (int i = lane; i < KW * (HD / 8); i += 32) {
               const int y = wn * KW + i / (HD / 8), pos = t * KT + y;
-              uint4* p = reinterpret_cast<uint4*>(sv + (at(va, y, i % (HD / 8)) - va));
+              uint4* p = reinterpret_cast<uint4*>(sv + chunk_at(y, i % (HD / 8)));
               if (pos >= q.len || !(landed >> (y / PR) & 1u)) {
                 *p = make_uint4(0, 0, 0, 0);
               } else if (scan && pos >= q.ctx) {
@@ -483,7 +486,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 #pragma unroll
               for (int d = 0; d < HD / 16; ++d) {
                 uint32_t b[4];
-                ldsm4t(at(va, wn * KW + j * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, d * 2 + ((lane >> 4) & 1)), b);
+                ldsm4t(va + v_row[j] + (d * 2 / (C::COLS / 8)) * col_bytes + ((d * 2 % (C::COLS / 8) * 16) ^ v_col), b);
                 mma16816<BF>(O[2 * d], p, b[0], b[1]);
                 mma16816<BF>(O[2 * d + 1], p, b[2], b[3]);
               }
@@ -503,7 +506,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 #pragma unroll
               for (int d = 0; d < HD / 8; ++d) {
                 const float2 v = unpack2<BF>(*reinterpret_cast<const uint32_t*>(
-                    sv + (at(va, wn * KW + y, d) - va) + c0 * 2));
+                    sv + chunk_at(wn * KW + y, d) + c0 * 2));
                 if (p0 != 0.f) { O[d][0] = fmaf(p0, v.x, O[d][0]); O[d][1] = fmaf(p0, v.y, O[d][1]); }
                 if (p1 != 0.f) { O[d][2] = fmaf(p1, v.x, O[d][2]); O[d][3] = fmaf(p1, v.y, O[d][3]); }
               }
@@ -516,9 +519,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 
         // ---------------------------------------- the states of a row block meet
 #pragma unroll
-        for (int half = WN; half >= 1; half >>= 1) {
-          if (part >= half && part < 2 * half) {
-            float* b = merge + (wm * half + part - half) * C::SLOT + lane;
+        for (int half = WN / 2; half >= 1; half >>= 1) {
+          if (wn >= half && wn < 2 * half) {
+            float* b = merge + (wm * half + wn - half) * C::SLOT + lane;
 #pragma unroll
             for (int d = 0; d < HD / 8; ++d)
 #pragma unroll
@@ -529,8 +532,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
             b[(HD / 2 + 3) * 32] = l[1];
           }
           asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-          if (part < half) {
-            const float* b = merge + (wm * half + part) * C::SLOT + lane;
+          if (wn < half) {
+            const float* b = merge + (wm * half + wn) * C::SLOT + lane;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float m2 = b[(HD / 2 + i) * 32], mn = fmaxf(m[i], m2);
@@ -548,7 +551,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           }
           asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         }
-        if (part == 0 && ok) {
+        if (wn == 0 && ok) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -687,12 +690,19 @@ static int block_rows(int hd, int64_t rows_per_head) {
 template <int HD, int KT, int BM, bool BF, class K>
 static int launch(K kern, int ctas, int threads, int smem, const TreeAttnArgs& a, const tl_kv_pool& p,
                   cudaStream_t s) {
-  constexpr int cols = HD < 64 ? HD : 64;
+  constexpr uint32_t cols = HD < 64 ? HD : 64;
+  constexpr CUtensorMapSwizzle sw = cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapDataType dt = BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap map;
   const uint64_t rows = (uint64_t)p.n_pages * 2 * p.n_kv_heads * p.page_tokens;
-  TL_TRY(encode_map_2d(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.dev_pool, HD,
-                       rows, HD * 2, cols, p.page_tokens < KT ? p.page_tokens : KT,
-                       cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+  const uint32_t pr = p.page_tokens < KT ? p.page_tokens : KT;
+  if (BM == 128) {  // boxes of 64 columns: the layout that the tensor core reads has positions next to one another
+    TL_TRY(encode_map_2d(&map, dt, p.dev_pool, HD, rows, HD * 2, cols, pr, sw));
+  } else {          // columns, positions, column tiles, K and V
+    TL_TRY(encode_map_4d(&map, dt, p.dev_pool, {cols, rows, HD / cols, 2},
+                         {HD * 2, cols * 2, (uint64_t)p.n_kv_heads * p.page_tokens * HD * 2}, {cols, pr, HD / cols, 2},
+                         sw));
+  }
   static uint64_t set = 0;  // per kernel: one bit per device
   int dev = 0;
   TL_CUDA(cudaGetDevice(&dev));
@@ -719,11 +729,11 @@ template <int HD, bool BF>
 static int run(const TreeAttnArgs& a, const tl_kv_pool& p, int n_sms, cudaStream_t s) {
   using C = Cfg<HD>;
   switch (block_rows(HD, (int64_t)a.max_nodes * (a.H / a.Hk))) {
-    case 16: return launch<HD, C::KT, 16, BF>(tree_attn_kernel<HD, 1, BF>, n_sms, kThreads, C::SMEM, a, p, s);
-    case 32: return launch<HD, C::KT, 32, BF>(tree_attn_kernel<HD, 2, BF>, n_sms, kThreads, C::SMEM, a, p, s);
+    case 16: return launch<HD, C::KT, 16, BF>(tree_attn_kernel<HD, 1, BF>, 2 * n_sms, kThreads, C::SMEM, a, p, s);
+    case 32: return launch<HD, C::KT, 32, BF>(tree_attn_kernel<HD, 2, BF>, 2 * n_sms, kThreads, C::SMEM, a, p, s);
     default:
       if constexpr (HD == 32)
-        return launch<HD, C::KT, 64, BF>(tree_attn_kernel<HD, 4, BF>, n_sms, kThreads, C::SMEM, a, p, s);
+        return launch<HD, C::KT, 64, BF>(tree_attn_kernel<HD, 4, BF>, 2 * n_sms, kThreads, C::SMEM, a, p, s);
       else
         return launch<HD, TcCfg<HD>::KT, 128, BF>(tree_attn_tc_kernel<HD, BF>, 2 * n_sms, TcCfg<HD>::THREADS,
                                                   TcCfg<HD>::SMEM, a, p, s);
@@ -741,7 +751,7 @@ static int sm_count(int* n) {
 
 size_t tree_attn_workspace(int hd, int64_t rows_per_head, int n_sms) {
   const int rows = tree::block_rows(hd, rows_per_head);
-  const size_t ctas = (size_t)n_sms * (rows == 128 ? 2 : 1);
+  const size_t ctas = 2 * (size_t)n_sms;
   return (ctas * sizeof(tree::Range) + 255) / 256 * 256 + ctas * 2 * rows * (hd + 2) * 4;
 }
 

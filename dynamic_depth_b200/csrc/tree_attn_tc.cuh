@@ -5,7 +5,7 @@
 // A row block is 128 query rows (one TMEM lane and one thread each), a tile 64
 // key positions:
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, into one of two
-//                  TMEM buffers
+//                  or three TMEM buffers
 //   P = exp2(S-m)  one thread a row; 16-bit P replaces S in its TMEM columns
 //   O += P V       tcgen05.mma with P as the TMEM operand A and V (rows of
 //                  keys) as the N-major operand B, accumulating in TMEM
@@ -40,8 +40,8 @@ struct TcCfg {
   static constexpr int STAGE = CT * TILE;          // K or V of a tile
   static constexpr int STAGES = HD == 128 ? 2 : 4; // of K, and of V
   static constexpr int Q_BYTES = BM * HD * 2;
-  static constexpr int SB = 2;                     // S buffers
-  static constexpr int TMEM_COLS = 256;            // S / P twice 64, O HD
+  static constexpr int SB = HD == 128 ? 2 : 3;     // S buffers
+  static constexpr int TMEM_COLS = 256;            // S / P two or three times 64, O HD
   static constexpr int THREADS = 256;
   static constexpr int SMEM = 1024 + Q_BYTES + 2 * STAGES * STAGE + 512;
   // two CTAs share an SM (and its 512 columns of TMEM), never three
@@ -125,7 +125,7 @@ __device__ __forceinline__ bool rows_any(bool v) {
   return r != 0;
 }
 
-// Tiles whose boxes are remembered: K runs at most STAGES tiles ahead of S, and S three ahead of the rows.
+// Tiles whose boxes are remembered: K runs at most STAGES tiles ahead of S, and S at most three ahead of the rows.
 constexpr int kInfo = 16;
 
 // A producer warp: K or V of the tiles of the CTA's range into its ring, a box
@@ -309,7 +309,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
         if (!(ok = mbar_wait_warp(smem_u32(q_full), seg & 1, abort_flag))) break;
         for (int t = s.t0; t < s.t1; ++t, ++k) {
           const int st = k % ST, buf = k % SB;
-          // P of tile k - 2 has been read from this buffer
+          // P of tile k - SB has been read from this buffer
           ok = (k < SB || mbar_wait_warp(smem_u32(&o_full[buf]), (k / SB - 1) & 1, abort_flag)) &&
                mbar_wait_warp(smem_u32(&k_full[st]), (k / ST) & 1, abort_flag);
           if (!ok) break;
@@ -426,7 +426,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
             const float mn = move ? mt : m, z = mn == -INFINITY ? 0.f : mn;
             if (t > s.t0 && __any_sync(0xffffffffu, move)) {
               const float corr = move ? ex2(m - z) : 1.f;
-              ok = mbar_wait_warp(smem_u32(&o_full[buf ^ 1]), ((k - 1) / SB) & 1, abort_flag);
+              ok = mbar_wait_warp(smem_u32(&o_full[(k - 1) % SB]), ((k - 1) / SB) & 1, abort_flag);
               tc_after();
               scale_o<HD>(to, corr);
               l *= corr;

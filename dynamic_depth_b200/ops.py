@@ -186,14 +186,24 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
     return q_out
 
 
+_workspace_sizes = {}
+
+
+def _workspace_bytes(hd, H, Hk, max_nodes, device_index):
+    key = (hd, H, Hk, max_nodes, device_index)
+    n = _workspace_sizes.get(key)
+    if n is None:
+        c = C.c_size_t()
+        check(lib().tl_tree_attention_workspace(hd, H, Hk, max_nodes, C.byref(c)), "tl_tree_attention_workspace")
+        n = _workspace_sizes[key] = c.value
+    return n
+
+
 def tree_attention_workspace(head_dim: int, n_heads: int, n_kv_heads: int, max_nodes: int, device="cuda"):
     """A workspace for tree_attention calls of these sizes (one per call that may run at the same time)."""
-    n = C.c_size_t()
-    dev = torch.device(device)
-    with _on(dev):
-        check(lib().tl_tree_attention_workspace(head_dim, n_heads, n_kv_heads, max_nodes, C.byref(n)),
-              "tl_tree_attention_workspace")
-        return _empty(torch.uint8, n.value)
+    on = _on(torch.device(device))
+    with on:
+        return _empty(torch.uint8, _workspace_bytes(head_dim, n_heads, n_kv_heads, max_nodes, on.index))
 
 
 def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=None, scale: float = 0.0, out=None,
@@ -225,10 +235,7 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
               and out.device == dev, "out: the shape of q, heads adjacent")
         lse = _empty(torch.float32, rows, H) if return_lse else None
         if workspace is None:
-            n = C.c_size_t()
-            check(lib().tl_tree_attention_workspace(hd, H, p.n_kv_heads, max_nodes, C.byref(n)),
-                  "tl_tree_attention_workspace")
-            workspace = _empty(torch.uint8, n.value)
+            workspace = _empty(torch.uint8, _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev.index))
         check(lib().tl_tree_attention(
             q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
             block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
