@@ -36,6 +36,8 @@ constexpr int kMaxTop = 64;
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
 constexpr int kCand = 2048;      // candidates ordered in shared memory; more take the extraction loop
+constexpr int kList = 256;       // chunks that reach the bound; more take the exact search
+constexpr int kWarpCand = 256;   // candidates of a row that one warp handles
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -244,85 +246,60 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return r;
 }
 
-struct Part {  // a CTA's share of a row
-  double S, T;
-  float m;
+// A part of a row: maximum, sums relative to it, tokens before the target.
+struct Part {
+  float m, S, T;
   int32_t before;
   int32_t nan;
 };
 
-// The lanes' (sum, weighted sum, maximum, count), joined; a NaN maximum marks a part that holds one.
-__device__ __forceinline__ Part merge_parts(double S, double T, float m, int before) {
+// The lanes' parts, joined.
+__device__ __forceinline__ Part merge_parts(const Part& q) {
   Part p;
-  p.nan = __any_sync(0xffffffffu, m != m);
-  p.m = warp_max(m != m ? -INFINITY : m);
-  const double d = (double)p.m - (double)m, k = m > -INFINITY ? exp(-d) : 0.0;
-  p.S = warp_sum_d(k * S);
-  p.T = warp_sum_d(m > -INFINITY ? k * (T - d * S) : 0.0);
-  p.before = __reduce_add_sync(0xffffffffu, before);
+  p.nan = __any_sync(0xffffffffu, q.nan);
+  p.m = warp_max(q.m);
+  const float d = p.m - q.m, k = q.m > -INFINITY ? expf(-d) : 0.f;
+  p.S = warp_sum(k * q.S);
+  p.T = warp_sum(k > 0.f ? k * (q.T - d * q.S) : 0.f);  // (d * S may be infinite where k is 0)
+  p.before = __reduce_add_sync(0xffffffffu, q.before);
   return p;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  extern __shared__ uint32_t leaders[];  // [n_chunks] chunk maxima; their sort keys from the search on
-  __shared__ Part part, merged;
-  __shared__ double wS[kWarps], wT[kWarps];
-  __shared__ float wm[kWarps];
-  __shared__ int32_t wcnt[kWarps];
-  __shared__ unsigned long long top[kMaxTop];               // this CTA's first n keys, in order
-  __shared__ unsigned long long cand[kCand];
-  __shared__ int32_t sel[kMaxTop];
-  __shared__ uint32_t tmax[kThreads];
-  __shared__ int32_t n_cand, n_sel, n_keys;
-  __shared__ uint32_t thr_key;
-  __shared__ unsigned long long best_w[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = cluster.num_blocks(), cr = cluster.block_rank();
-  const int64_t r = blockIdx.x / cs;
-  const int V = a.V, n_top = a.n_top;
-  const T* row = reinterpret_cast<const T*>(a.x) + r * a.stride;
-  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-  const int all_chunks = (V + lead + kChunk - 1) / kChunk;
-  // whole groups of U chunks per CTA; those past the row's end read as -inf
-  constexpr int U = 4 / Raw<T>::W;
-  const int per = ((all_chunks + cs - 1) / cs + U - 1) / U * U;
-  const int c0 = min(all_chunks, per * cr), c1 = min(all_chunks, c0 + per), nc = c1 - c0;
-  const int t = a.targets ? a.targets[r] : -1;
-  const bool has_t = t >= 0 && t < V;
-  const float xt = has_t ? to_f<T>(row[t]) : 0.f;
-
-  // ------------------------------------------------------------ one pass
-  // U chunks of a warp at a time (64 bytes a lane), the next U on their way meanwhile.
+// One pass of a warp over chunks cb, cb + step, ... below c1 of a row, U at a
+// time (64 bytes a lane) with the next U on their way meanwhile; lead_fn(chunk,
+// maximum) hears of every chunk.  mine: the lane's largest element of the even
+// and of the odd chunks of its groups.
+template <class T, int U, class F>
+__device__ __forceinline__ Part stream_chunks(const T* row, int lead, int V, int t, float xt, bool has_t, int cb, int c1,
+                                              int step, int lane, float (&mine)[2], F lead_fn) {
   float m = -INFINITY;
   F2 S2 = f2(0.f, 0.f), T2 = f2(0.f, 0.f);
   int before = 0;
   bool nan = false;
-  float mine = -INFINITY;  // the thread's largest element
+  mine[0] = mine[1] = -INFINITY;
   const F2 log2e = f2(kLog2e, kLog2e);
   Raw<T> next[U];
-  load_group<T, U>(next, row, lead, V, c0 + warp * U, lane);
-  for (int cb = c0 + warp * U; cb < c1; cb += kWarps * U) {
+  load_group<T, U>(next, row, lead, V, cb, lane);
+  for (; cb < c1; cb += step) {
     Raw<T> cur[U];
     float cm[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) cur[u] = next[u];
-    if (cb + kWarps * U < c1) load_group<T, U>(next, row, lead, V, cb + kWarps * U, lane);
+    if (cb + step < c1) load_group<T, U>(next, row, lead, V, cb + step, lane);
     float top_m = -INFINITY;  // NaN if one is
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float lm = max8<T>(cur[u]);
-      mine = max_nan(mine, lm);
+      mine[u & 1] = max_nan(mine[u & 1], lm);
       cm[u] = warp_max_nan(lm);
-      if (lane == 0) leaders[cb + u - c0] = __float_as_uint(cm[u]);
+      lead_fn(cb + u, cm[u]);
       top_m = u == 0 ? cm[0] : max_nan(top_m, cm[u]);
     }
     if (!(top_m <= m)) {
       nan |= top_m != top_m;
+      // (from -inf, or so far that nothing is left of the sums, the difference itself must not enter them)
       const float d = top_m - m, k = m == -INFINITY ? 0.f : ex2(-d * kLog2e);
-      const F2 kk = f2(k, k), dd = m == -INFINITY ? f2(0.f, 0.f) : f2(-d, -d);
+      const F2 kk = f2(k, k), dd = k == 0.f ? f2(0.f, 0.f) : f2(-d, -d);
       T2 = mul2(kk, fma2(dd, S2, T2));
       S2 = mul2(kk, S2);
       m = fmaxf(m, top_m);  // past a NaN the sums mean nothing
@@ -380,115 +357,246 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
       }
     }
   }
-  {
-    float s0, s1, t0, t1;
-    f2_out(S2, s0, s1);
-    f2_out(T2, t0, t1);
-    const double s = warp_sum_d((double)s0 + (double)s1), u = warp_sum_d((double)t0 + (double)t1);
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) { wS[warp] = s; wT[warp] = u; wm[warp] = nan ? __uint_as_float(0x7fc00000u) : m; wcnt[warp] = before; }
+  float s0, s1, t0, t1;
+  f2_out(S2, s0, s1);
+  f2_out(T2, t0, t1);
+  Part p;
+  p.m = m;
+  p.S = warp_sum(s0 + s1);
+  p.T = warp_sum(t0 + t1);
+  p.before = __reduce_add_sync(0xffffffffu, before);
+  p.nan = nan;
+  return p;
+}
+
+// The n-th largest of 32 (n <= 20) or 64 group maxima, two a lane: a bound with n elements at or above it.
+__device__ __forceinline__ uint32_t nth_bound(uint32_t g0, uint32_t g1, int n, int lane) {
+  if (n <= 20) {
+    const uint32_t g = max(g0, g1);
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t o = __shfl_sync(0xffffffffu, g, j);
+      rank += o > g || (o == g && j < lane);
+    }
+    return __reduce_max_sync(0xffffffffu, rank == n - 1 ? g : 0u);
   }
-  tmax[threadIdx.x] = sort_key(mine);
-  if (threadIdx.x == 0) n_cand = 0;
+  int r0 = 0, r1 = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t a0 = __shfl_sync(0xffffffffu, g0, j), a1 = __shfl_sync(0xffffffffu, g1, j);
+    r0 += (a0 > g0 || (a0 == g0 && j < lane)) + (a1 > g0);
+    r1 += (a0 >= g1) + (a1 > g1 || (a1 == g1 && j < lane));
+  }
+  return __reduce_max_sync(0xffffffffu, max(r0 == n - 1 ? g0 : 0u, r1 == n - 1 ? g1 : 0u));
+}
+
+// Adds the lane's elements that reach b, a number above -inf (NaN reaches it,
+// the -inf outside the row does not), to the candidates: (key, ~id), in any
+// order.  Most lanes hold none; the others take them one by one.
+template <class T>
+__device__ __forceinline__ void add_reaching(const Raw<T>& raw, int pos0, int lead, int lane, float b,
+                                             unsigned long long* cand, int cap, int* n_cand) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(raw.w);
+  uint32_t in = 0;  // bit e: element e
+  if constexpr (sizeof(T) == 4) {
+    bool below = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) below &= __uint_as_float(u[i]) < b;
+    if (below) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) in |= (uint32_t)!(__uint_as_float(u[i]) < b) << i;
+  } else {
+    typedef typename Word<T>::V2 V2;
+    const V2 bb = Word<T>::both(b);
+    const V2* v = reinterpret_cast<const V2*>(u);
+    const uint32_t l0 = __hlt2_mask(v[0], bb), l1 = __hlt2_mask(v[1], bb), l2 = __hlt2_mask(v[2], bb),
+                   l3 = __hlt2_mask(v[3], bb);
+    if ((l0 & l1 & l2 & l3) == ~0u) return;
+    // one bit of each half word, side by side
+    in = (~l0 & 0x00020001u) | (~l1 & 0x00080004u) | (~l2 & 0x00200010u) | (~l3 & 0x00800040u);
+    in = (in | in >> 16) & 0xffu;
+  }
+  int at = atomicAdd(n_cand, __popc(in));
+  do {
+    const int e = __ffs(in) - 1;
+    in &= in - 1;
+    float x;
+    if constexpr (sizeof(T) == 4) {
+      uint32_t w = u[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) w = e == i ? u[i] : w;
+      x = __uint_as_float(w);
+    } else {
+      const uint32_t w = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
+      const float2 f = Word<T>::two(w);
+      x = e & 1 ? f.y : f.x;
+    }
+    if (at < cap)
+      cand[at] = (unsigned long long)sort_key(x) << 32 | (0xffffffffu - (uint32_t)elem_index<T>(pos0, lead, lane, e));
+    ++at;
+  } while (in);
+}
+
+// Adds the chunk's elements above key `tk`, and of those equal to it the first
+// `ties` (which it lowers), to the candidates: (key, ~id), in any order.
+template <class T>
+__device__ __forceinline__ void add_candidates(const Raw<T>& raw, int pos0, int lead, int V, int lane, uint32_t tk,
+                                               int* ties, unsigned long long* cand, int cap, int* n_cand) {
+  constexpr int E = 16 / sizeof(T);
+  uint32_t in = 0, eq = 0;
+  float f[8];
+  unpack<T>(raw, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int id = elem_index<T>(pos0, lead, lane, e);
+    const uint32_t k = sort_key(f[e]);
+    const bool real = id >= 0 && id < V;
+    in |= (uint32_t)(real && k > tk) << e;
+    eq |= (uint32_t)(real && k == tk) << e;
+  }
+  if (__any_sync(0xffffffffu, eq)) {
+    int left = *ties;
+#pragma unroll
+    for (int w = 0; w < 8 / E; ++w) {  // by id: word after word, lane after lane
+      uint32_t mine = eq >> (w * E) & ((1u << E) - 1u);
+      const int n = __popc(mine);
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      for (int keep = left - (x - n); mine && keep > 0; --keep) {
+        in |= (mine & -mine) << (w * E);
+        mine &= mine - 1;
+      }
+      left -= __shfl_sync(0xffffffffu, x, 31);
+    }
+    *ties = max(left, 0);
+  }
+  if (in) {
+    int at = atomicAdd(n_cand, __popc(in));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (in >> e & 1u) {
+        const uint32_t id = (uint32_t)elem_index<T>(pos0, lead, lane, e);
+        if (at < cap) cand[at] = (unsigned long long)sort_key(f[e]) << 32 | (0xffffffffu - id);
+        ++at;
+      }
+  }
+  __syncwarp();
+}
+
+// The outputs of one row from its joined part.
+struct RowOut {
+  float m, lnS, xt;
+  bool bad, none;
+  __device__ __forceinline__ RowOut(const Part& p) {
+    m = p.m;
+    bad = p.nan || p.m == INFINITY;
+    none = p.m == -INFINITY;
+    lnS = none || bad ? 0.f : logf(p.S);
+  }
+  __device__ __forceinline__ float lp(float x) const {
+    return bad ? __uint_as_float(0x7fc00000u) : (x == -INFINITY ? -INFINITY : (x - m) - lnS);
+  }
+  __device__ __forceinline__ void write(const Args& a, int64_t r, const Part& p, int t, bool has_t, float xt) const {
+    const float qnan = __uint_as_float(0x7fc00000u);
+    if (a.logprob) a.logprob[r] = has_t ? lp(xt) : (t == -1 ? 0.f : qnan);
+    if (a.rank) a.rank[r] = has_t && !p.nan ? p.before : -1;
+    if (a.entropy) a.entropy[r] = bad ? qnan : (none ? 0.f : lnS - p.T / p.S);
+    if (a.lse) a.lse[r] = bad ? qnan : (none ? -INFINITY : m + lnS);
+  }
+  __device__ __forceinline__ void write_top(const Args& a, int64_t r, int i, unsigned long long k) const {
+    if (a.top_ids) a.top_ids[r * a.n_top + i] = (int32_t)(0xffffffffu - (uint32_t)k);
+    if (a.top_lp) a.top_lp[r * a.n_top + i] = lp(key_value((uint32_t)(k >> 32)));
+  }
+};
+
+// A CTA, or a cluster of CTAs, a row.  CTAs an SM: four of fp32 rows (500 x
+// 131072: 51 us, against 65 with three), three of 16-bit rows, whose unpacking
+// takes more registers (1000 x 131072, n 20: 62 us, against 68 with four).
+template <class T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) logprobs_kernel(Args a) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ uint32_t leaders[];  // [n_chunks] chunk maxima; their sort keys from an exact search on
+  __shared__ Part part, wpart[kWarps];
+  __shared__ unsigned long long top[kMaxTop];               // this CTA's first n keys, in order
+  __shared__ unsigned long long cand[kCand];
+  __shared__ int32_t sel[kMaxTop], list[kList];
+  __shared__ uint32_t tmax[2][kThreads];
+  __shared__ int32_t n_cand, n_sel, n_keys, n_list;
+  __shared__ uint32_t thr_key;
+  __shared__ unsigned long long best_w[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = cluster.num_blocks(), cr = cluster.block_rank();
+  const int64_t r = blockIdx.x / cs;
+  const int V = a.V, n_top = a.n_top;
+  const T* row = reinterpret_cast<const T*>(a.x) + r * a.stride;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int all_chunks = (V + lead + kChunk - 1) / kChunk;
+  // whole groups of U chunks per CTA; those past the row's end read as -inf
+  constexpr int U = 4 / Raw<T>::W;
+  const int per = ((all_chunks + cs - 1) / cs + U - 1) / U * U;
+  const int c0 = min(all_chunks, per * cr), c1 = min(all_chunks, c0 + per), nc = c1 - c0;
+  const int t = a.targets ? a.targets[r] : -1;
+  const bool has_t = t >= 0 && t < V;
+  const float xt = has_t ? to_f<T>(row[t]) : 0.f;
+  float mine[2];
+  if (threadIdx.x == 0) n_cand = n_list = 0;
+  {
+    const Part p = stream_chunks<T, U>(row, lead, V, t, xt, has_t, c0 + warp * U, c1, kWarps * U, lane, mine,
+                                       [&](int c, float cm) { if (lane == 0) leaders[c - c0] = __float_as_uint(cm); });
+    if (lane == 0) wpart[warp] = p;
+  }
+  tmax[0][threadIdx.x] = sort_key(mine[0]);
+  tmax[1][threadIdx.x] = sort_key(mine[1]);
   __syncthreads();
-  if (warp == 1) {  // beside warp 0's search: lane w takes warp w's sums
-    const bool in = lane < kWarps;
-    const Part p = merge_parts(in ? wS[lane] : 0.0, in ? wT[lane] : 0.0, in ? wm[lane] : -INFINITY,
-                               in ? wcnt[lane] : 0);
+  if (warp == kWarps - 1) {  // lane w takes warp w's part
+    const Part p = merge_parts(lane < kWarps ? wpart[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0});
     if (lane == 0) part = p;
   }
 
   // ------------------------------------- the first n_top keys of this CTA's part
   if (n_top > 0) {
-    // A bound from disjoint groups of elements: the n_top-th largest of 32 (or
-    // 64) group maxima has n_top elements at or above it.  Every warp finds it
-    // from the threads' maxima, then takes the elements at or above it from the
-    // chunks whose maxima reach it.
+    // every warp finds the bound from the threads' maxima and lists its share of the chunks that reach it
     uint32_t g0 = 0, g1 = 0;
 #pragma unroll
-    for (int j = 0; j < kWarps; j += 2) {
-      g0 = max(g0, tmax[j * 32 + lane]);
-      g1 = max(g1, tmax[j * 32 + 32 + lane]);
+    for (int j = 0; j < kWarps; ++j) {
+      g0 = max(g0, tmax[0][j * 32 + lane]);
+      g1 = max(g1, tmax[1][j * 32 + lane]);
     }
-    uint32_t bound;
-    if (n_top <= 20) {
-      const uint32_t g = max(g0, g1);
-      int rank = 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t o = __shfl_sync(0xffffffffu, g, j);
-        rank += o > g || (o == g && j < lane);
-      }
-      bound = __reduce_max_sync(0xffffffffu, rank == n_top - 1 ? g : 0u);
-    } else {
-      int r0 = 0, r1 = 0;
-#pragma unroll 4
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t a0 = __shfl_sync(0xffffffffu, g0, j), a1 = __shfl_sync(0xffffffffu, g1, j);
-        r0 += (a0 > g0 || (a0 == g0 && j < lane)) + (a1 > g0);
-        r1 += (a0 >= g1) + (a1 > g1 || (a1 == g1 && j < lane));
-      }
-      bound = __reduce_max_sync(0xffffffffu, max(r0 == n_top - 1 ? g0 : 0u, r1 == n_top - 1 ? g1 : 0u));
-    }
-    // adds the elements of chunk c at or above key `tk` (among equals, the first `ties` of the chunk)
-    auto gather = [&](int c, uint32_t tk, int ties) {
-      float f[8];
-      const int pos0 = (c0 + c) * kChunk;
-      load8<T>(row, lead, V, pos0, lane, f);
-      constexpr int E = 16 / sizeof(T);
-      uint32_t eq = 0;
-      int rank = 0;  // equals of the chunk before the lane's, word by word
-      if (ties < kChunk) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int id = elem_index<T>(pos0, lead, lane, e);
-          eq |= (uint32_t)(id >= 0 && id < V && sort_key(f[e]) == tk) << e;
-        }
-      }
-      uint32_t in = 0;
-      int words = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (ties < kChunk && e % E == 0) {
-          const int n = __popc(eq >> e & ((1u << E) - 1u));
-          int x = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          rank = words + x - n;
-          words += __shfl_sync(0xffffffffu, x, 31);
-        }
-        const int id = elem_index<T>(pos0, lead, lane, e);
-        const uint32_t k = sort_key(f[e]);
-        bool take = id >= 0 && id < V && k >= tk;
-        if (ties < kChunk && k == tk) take = take && rank++ < ties;
-        in |= (uint32_t)take << e;
-      }
-      if (in) {  // few lanes
-        int at = atomicAdd(&n_cand, __popc(in));  // any order: the keys hold the ids
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (in >> e & 1u) {
-            const uint32_t id = (uint32_t)elem_index<T>(pos0, lead, lane, e);
-            if (at < kCand) cand[at] = (unsigned long long)sort_key(f[e]) << 32 | (0xffffffffu - id);
-            ++at;
-          }
-      }
-      __syncwarp();
-    };
-    for (int i = 0; i < nc; i += kThreads) {  // the warps take chunks in turn
+    const uint32_t bound = nth_bound(g0, g1, n_top, lane);
+    const float b = key_value(bound);
+    const bool plain = b > -INFINITY;  // else masked rows, or NaN: the exact form
+    for (int i = 0; plain && i < nc; i += kThreads) {
       const int c = i + lane * kWarps + warp;
-      unsigned reach = __ballot_sync(0xffffffffu, c < nc && sort_key(__uint_as_float(leaders[c])) >= bound);
-      while (reach) {
-        gather(i + (__ffs(reach) - 1) * kWarps + warp, bound, kChunk);
-        reach &= reach - 1;
+      if (c < nc && sort_key(__uint_as_float(leaders[c])) >= bound) {
+        const int at = atomicAdd(&n_list, 1);
+        if (at < kList) list[at] = c;
+      }
+    }
+    __syncthreads();
+    const int nl = n_list;
+    if (nl <= kList) {  // four chunks of a warp at a time, loaded together
+      for (int i = warp * 4; i < nl; i += kWarps * 4) {
+        Raw<T> raw[4];
+        int c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          c[u] = i + u < nl ? list[i + u] : -1;
+          if (c[u] >= 0) raw[u] = load_raw<T>(row, lead, V, (c0 + c[u]) * kChunk, lane);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c[u] >= 0) add_reaching<T>(raw[u], (c0 + c[u]) * kChunk, lead, lane, b, cand, kCand, &n_cand);
       }
     }
     __syncthreads();
     int ns = 0;
-    if (n_cand > kCand) {
+    if (!plain || nl > kList || n_cand > kCand) {
       // Many at the bound (masked or constant rows) or few chunks holding all the best: the n_top first chunks
       // exactly, in the order of their maxima; of elements equal to the last one's, n_top of a chunk at most.
       __syncthreads();
@@ -522,7 +630,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
       __syncthreads();
       ns = n_sel;
       const uint32_t tk = thr_key;
-      for (int i = warp; i < ns; i += kWarps) gather(sel[i], tk, n_top);
+      for (int i = warp; i < ns; i += kWarps) {
+        int ties = n_top;
+        add_candidates<T>(load_raw<T>(row, lead, V, (c0 + sel[i]) * kChunk, lane), (c0 + sel[i]) * kChunk, lead, V, lane,
+                          tk, &ties, cand, kCand, &n_cand);
+      }
     }
     __syncthreads();
     const int n = n_cand, out = min(n_top, n);
@@ -532,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
         for (int i = threadIdx.x; i < n; i += kThreads) {
           const unsigned long long k = cand[i];
           int rank = 0;
+#pragma unroll 4
           for (int j = 0; j < n; ++j) rank += cand[j] > k;
           if (rank < out) top[rank] = k;
         }
@@ -554,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
         for (int i = threadIdx.x; i < out; i += kThreads) top[i] = cand[i];
       }
     } else {
-      // many equal or ascending values: extract one after another
+      // many ascending values: extract one after another
       unsigned long long last = ~0ull;
       for (int o = 0; o < out; ++o) {
         unsigned long long best = 0;
@@ -583,13 +696,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
         __syncthreads();
       }
     }
-    __syncthreads();
     if (threadIdx.x == 0) n_keys = out;
   }
 
   // ------------------------------------------------- merge over the cluster
   if (cs > 1) {
     cluster.sync();
+    Part all{};
     if (cr == 0) {
       // the lists, one behind the other: the rank of a key is the keys above it in every list
       if (n_top > 0) {
@@ -597,51 +710,132 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
           const int b = i / n_top, j = i % n_top;
           cand[i] = j < *cluster.map_shared_rank(&n_keys, b) ? cluster.map_shared_rank(top, b)[j] : 0ull;
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < cs * n_top; i += kThreads) {
-          const unsigned long long k = cand[i];
-          if (k == 0ull) continue;
-          int rank = 0;
-          for (int b = 0; b < cs; ++b) {
-            int lo = 0, hi = n_top;  // keys of list b above k
-            while (lo < hi) {
-              const int mid = (lo + hi) >> 1;
-              if (cand[b * n_top + mid] > k) lo = mid + 1; else hi = mid;
-            }
-            rank += lo;
-          }
-          if (rank < n_top) top[rank] = k;
+      }
+      all = merge_parts(lane < cs ? *cluster.map_shared_rank(&part, lane) : Part{-INFINITY, 0.f, 0.f, 0, 0});
+    }
+    cluster.sync();  // the other CTAs are done
+    if (cr != 0) return;
+    const RowOut o(all);
+    if (threadIdx.x == 0) o.write(a, r, all, t, has_t, xt);
+    for (int i = threadIdx.x; i < cs * n_top; i += kThreads) {
+      const unsigned long long k = cand[i];
+      if (k == 0ull) continue;
+      int rank = 0;
+      for (int b = 0; b < cs; ++b) {
+        int lo = 0, hi = n_top;  // keys of list b above k
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (cand[b * n_top + mid] > k) lo = mid + 1; else hi = mid;
+        }
+        rank += lo;
+      }
+      if (rank < n_top) o.write_top(a, r, rank, k);
+    }
+    return;
+  }
+  __syncthreads();
+  const Part p = part;
+  const RowOut o(p);
+  if (threadIdx.x == 0) o.write(a, r, p, t, has_t, xt);
+  for (int i = threadIdx.x; i < n_top; i += kThreads) o.write_top(a, r, i, top[i]);
+}
+
+// A warp a row, for many rows of up to 64 chunks: everything stays in the warp,
+// with no barrier.  4000 rows of 8000 bf16 logits, n 20: 37 us, against 60 us
+// with a CTA a row, whose end (several barriers a row) outweighs the row.
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_warp_kernel(Args a) {
+  __shared__ unsigned long long cand_s[kWarps][kWarpCand];
+  __shared__ int32_t n_cand_s[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  if (r >= a.rows) return;
+  const int V = a.V, n_top = a.n_top;
+  const T* row = reinterpret_cast<const T*>(a.x) + r * a.stride;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int nc = (V + lead + kChunk - 1) / kChunk;
+  constexpr int U = 4 / Raw<T>::W;
+  const int t = a.targets ? a.targets[r] : -1;
+  const bool has_t = t >= 0 && t < V;
+  const float xt = has_t ? to_f<T>(row[t]) : 0.f;
+  unsigned long long* cand = cand_s[warp];
+  int* n_cand = &n_cand_s[warp];
+  if (lane == 0) *n_cand = 0;
+  float mine[2], lead_max[2] = {-INFINITY, -INFINITY};  // lane l: the maxima of chunks l and l + 32
+  const Part p = stream_chunks<T, U>(row, lead, V, t, xt, has_t, 0, nc, U, lane, mine, [&](int c, float cm) {
+    lead_max[0] = c == lane ? cm : lead_max[0];
+    lead_max[1] = c == lane + 32 ? cm : lead_max[1];
+  });
+  const RowOut o(p);
+  if (lane == 0) o.write(a, r, p, t, has_t, xt);
+  if (n_top == 0) return;
+  const uint32_t bound = nth_bound(sort_key(mine[0]), sort_key(mine[1]), n_top, lane);
+  const uint32_t reach[2] = {
+      __ballot_sync(0xffffffffu, lane < nc && sort_key(lead_max[0]) >= bound),
+      __ballot_sync(0xffffffffu, lane + 32 < nc && sort_key(lead_max[1]) >= bound)};
+  // four chunks at a time, loaded together
+  auto each = [&](auto fn) {
+    uint64_t left = (uint64_t)reach[1] << 32 | reach[0];
+    while (left) {
+      Raw<T> raw[4];
+      int c[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        c[u] = left ? __ffsll((long long)left) - 1 : -1;
+        left &= left - 1;
+        if (c[u] >= 0) raw[u] = load_raw<T>(row, lead, V, c[u] * kChunk, lane);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c[u] >= 0) fn(raw[u], c[u] * kChunk);
+    }
+    __syncwarp();
+  };
+  const float b = key_value(bound);
+  const bool plain = b > -INFINITY;
+  if (plain) each([&](const Raw<T>& w, int pos0) { add_reaching<T>(w, pos0, lead, lane, b, cand, kWarpCand, n_cand); });
+  if (!plain || *n_cand > kWarpCand) {
+    // masked or constant rows: chunks in the order of ids, so no more than n_top equals of the bound are among the first
+    __syncwarp();
+    if (lane == 0) *n_cand = 0;
+    __syncwarp();
+    int ties = n_top;
+    each([&](const Raw<T>& w, int pos0) {
+      add_candidates<T>(w, pos0, lead, V, lane, bound, &ties, cand, kWarpCand, n_cand);
+    });
+  }
+  const int n = *n_cand;
+  if (n <= kWarpCand) {
+    for (int i = lane; i < n; i += 32) {
+      const unsigned long long k = cand[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += cand[j] > k;
+      if (rank < n_top) o.write_top(a, r, rank, k);
+    }
+  } else {  // many above the bound (ascending values): extract one after another
+    unsigned long long last = ~0ull;
+    for (int i = 0; i < n_top; ++i) {
+      unsigned long long best = 0;
+      for (int c = 0; c < nc; ++c) {
+        if (!(reach[c >> 5] >> (c & 31) & 1u)) continue;
+        float f[8];
+        load8<T>(row, lead, V, c * kChunk, lane, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int id = elem_index<T>(c * kChunk, lead, lane, e);
+          const unsigned long long k = (unsigned long long)sort_key(f[e]) << 32 | (0xffffffffu - (uint32_t)id);
+          if (id >= 0 && id < V && k < last && k > best) best = k;
         }
       }
-      if (warp == 1) {
-        Part q{0.0, 0.0, -INFINITY, 0, 0};
-        if (lane < cs) q = *cluster.map_shared_rank(&part, lane);
-        const Part p = merge_parts(q.S, q.T, q.nan ? __uint_as_float(0x7fc00000u) : q.m, q.before);
-        if (lane == 0) merged = p;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, s);
+        best = k > best ? k : best;
       }
+      last = best;
+      if (lane == 0) o.write_top(a, r, i, best);
     }
-    cluster.sync();
-  } else {
-    __syncthreads();
-  }
-  if (cr != 0) return;
-
-  // ------------------------------------------------------------- outputs
-  const Part p = cs > 1 ? merged : part;
-  const bool bad = p.nan || p.m == INFINITY, none = p.m == -INFINITY;
-  const float qnan = __uint_as_float(0x7fc00000u);
-  const double lnS = none || bad ? 0.0 : log(p.S);
-  auto lp = [&](float x) { return bad ? qnan : (x == -INFINITY ? -INFINITY : (float)((double)x - (double)p.m - lnS)); };
-  if (threadIdx.x == 0) {
-    if (a.logprob) a.logprob[r] = has_t ? lp(xt) : (t == -1 ? 0.f : qnan);
-    if (a.rank) a.rank[r] = has_t && !p.nan ? p.before : -1;
-    if (a.entropy) a.entropy[r] = bad ? qnan : (none ? 0.f : (float)(lnS - p.T / p.S));
-    if (a.lse) a.lse[r] = bad ? qnan : (none ? -INFINITY : (float)((double)p.m + lnS));
-  }
-  for (int i = threadIdx.x; i < n_top; i += kThreads) {
-    const unsigned long long k = top[i];
-    if (a.top_ids) a.top_ids[r * n_top + i] = (int32_t)(0xffffffffu - (uint32_t)k);
-    if (a.top_lp) a.top_lp[r * n_top + i] = lp(key_value((uint32_t)(k >> 32)));
   }
 }
 
@@ -650,9 +844,12 @@ static int launch(Args a, cudaStream_t s) {
   int dev = 0, sms = 0;
   TL_CUDA(cudaGetDevice(&dev));
   TL_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  // CTAs of a row: enough for four on every SM, each with 8 chunks or more
+  // many short rows: a warp a row
+  const bool by_warp = a.V + 8 <= 64 * kChunk && a.rows >= 8 * sms;
+  // CTAs of a row: as many as fill the SMs at most once (a second wave of them costs more than the first saves:
+  // 128 x 131072 bf16 took 16 us with 2 CTAs a row and 31 us with 8), each with 2 groups of chunks a warp or more
   int cs = 1;
-  while (cs < kMaxCluster && a.rows * cs < 4 * sms && a.V >= 2 * cs * kWarps * kChunk) cs *= 2;
+  while (cs < kMaxCluster && a.rows * cs * 2 <= 3 * sms && a.V >= 2 * cs * kWarps * kChunk) cs *= 2;
   const int chunks = (a.V + 8 + kChunk - 1) / kChunk;
   a.n_chunks = (chunks + cs - 1) / cs + 4;  // rounded up to groups of 4 at most
   const int64_t most = 0x7fffffff / kMaxCluster;  // rows of one launch
@@ -667,6 +864,12 @@ static int launch(Args a, cudaStream_t s) {
     if (b.lse) b.lse += r0;
     if (b.top_ids) b.top_ids += r0 * a.n_top;
     if (b.top_lp) b.top_lp += r0 * a.n_top;
+    if (by_warp) {
+      const int wpc = kWarps;
+      logprobs_warp_kernel<T><<<(unsigned)((b.rows + wpc - 1) / wpc), wpc * 32, 0, s>>>(b);
+      TL_CUDA(cudaGetLastError());
+      continue;
+    }
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(b.rows * cs));
     lc.blockDim = dim3(kThreads);

@@ -71,6 +71,54 @@ def test_logprobs_structured_rows(dtype):
     check_logprobs(x, torch.tensor([0, -1, 3, 5999, 5999, 0, 0, 302, 0], device="cuda").int(), 3)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,vocab", [(3, 40000), (1500, 9000)])
+def test_logprobs_masks_of_the_lowest_value(dtype, rows, vocab):
+    """Masked stretches (the type's lowest value, or -inf) before and after the tokens that are left, in every order
+    that a pass over the row can meet them; a warp a row and a cluster a row."""
+    g = gen(vocab)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 4).to(dtype)
+    low = torch.finfo(dtype).min
+    x[0, :vocab * 3 // 4] = low
+    x[1, vocab // 8:] = low
+    x[2, :vocab // 2] = -math.inf
+    x[2, vocab // 2:-3] = low
+    pick = torch.tensor([vocab - 1, 5, vocab - 2] + [vocab // 2] * (rows - 3), device="cuda").int()
+    o = T.token_logprobs(x, pick, n_top=7)
+    check_logprobs(x[:3], pick[:3], 7)
+    small = T.token_logprobs(x[:3].contiguous(), pick[:3].contiguous(), n_top=7)
+    for u, v in zip(o, small):  # either way of sharing the rows out: the same ids, sums to rounding
+        assert torch.equal(u[:3], v) if v.dtype == torch.int32 else torch.allclose(u[:3], v, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("n_top", [1, 20, 21, 64])
+def test_logprobs_many_short_rows(n_top):
+    """A warp a row: random rows, and rows whose values are all equal, ascending, or mostly masked."""
+    V, rows = 3001, 1300
+    x = torch.randn(rows, V, generator=gen(n_top), device="cuda") * 3
+    x[0] = 1.0
+    x[1] = torch.arange(V, device="cuda")
+    x[2] = -torch.arange(V, device="cuda")
+    x[3] = -math.inf
+    x[4, 7:] = -math.inf
+    x[5] = (torch.arange(V, device="cuda") // 300).float()
+    x[6, 2990:] = math.nan
+    t = torch.randint(0, V, (rows,), generator=gen(1), device="cuda").int()
+    keep = list(range(12)) + [rows - 1]
+    for dtype in (F32, BF16):
+        y = x.to(dtype)
+        o = T.token_logprobs(y, t, n_top=n_top)
+        tol = R.sum_bound(V / 32 + 8)  # a lane sums at most vocab / 32 terms
+        for r in keep:
+            lp, rank, ent, lse, ids, top = R.logprobs_row(y[r].double().cpu().numpy(), int(t[r]), n_top)
+            assert o.top_ids[r].tolist() == ids.tolist() and int(o.rank[r]) == rank
+            for got, want in ((o.logprob[r], lp), (o.lse[r], lse), (o.entropy[r], ent)):
+                assert np.allclose(float(got), want, rtol=2.0 ** -23, equal_nan=True,
+                                   atol=2 * tol * (1 + abs(ent)) if math.isfinite(want) else 0)
+            assert np.allclose(o.top_logprobs[r].cpu().double().numpy(), top, rtol=2.0 ** -23, atol=2 * tol,
+                               equal_nan=True)
+
+
 def test_logprobs_nan_and_infinity():
     x = torch.randn(5, 3001, generator=gen(3), device="cuda")
     x[0, 17] = math.nan
