@@ -73,9 +73,29 @@ struct Range {
   int64_t u0, u1;   // units of this CTA
   int64_t base;     // first unit of the request that holds u0
   int64_t ua, ub;   // units of the row block that holds u0
-  int32_t r, hk, blk, pad;
+  int64_t total;    // units in all
+  int32_t r, hk, blk;
+  // the CTAs with pieces of the row block that u0 cuts, first to last (between them some may have no units, where
+  // there are fewer units than CTAs); -1: u0 cuts none, or it is not the block's first cut
+  int32_t cut_first, cut_last;
   Req q;
 };
+// What the joining kernel needs beyond the range itself; thread 0 notes it when the CTA's work is done.
+__device__ __forceinline__ void note_cut(const TreeAttnArgs& a, const Range& me) {
+  Range* out = reinterpret_cast<Range*>(a.ws) + blockIdx.x;
+  const uint64_t U = me.total, G = gridDim.x;
+  auto owner = [&](uint64_t u) { return (int)(((u + 1) * G - 1) / U); };  // the CTA whose range holds u
+  int first = -1, last = -1;
+  if (me.u0 < me.u1 && me.u0 > me.ua) {
+    const int p = owner(me.ua);
+    if (owner(me.u0 - 1) == p) {
+      first = p;
+      last = owner(me.ub - 1);
+    }
+  }
+  out->cut_first = first;
+  out->cut_last = last;
+}
 
 // A piece of a row block in the workspace: (maximum, sum) of each row, then the
 // output as [hd / 4][BM] groups of four values, so that neighbouring rows are
@@ -188,7 +208,7 @@ struct Walk {
 template <int KT, int BM>
 __device__ __forceinline__ void find_range(const TreeAttnArgs& a, Range* sh, long long* wsum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long total = 0, u0 = 0, u1 = 0;
+  long long all = 0, u0 = 0, u1 = 0;
   for (int pass = 0; pass < 2; ++pass) {
     long long run = 0;
     for (int r0 = 0; r0 < a.R; r0 += blockDim.x) {
@@ -215,21 +235,22 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, Range* sh, lon
         run += wsum[w];
       }
       if (a.R <= (int)blockDim.x) {
-        u0 = run * blockIdx.x / gridDim.x;
-        u1 = run * (blockIdx.x + 1) / gridDim.x;
+        all = run;
+        u0 = all * blockIdx.x / gridDim.x;
+        u1 = all * (blockIdx.x + 1) / gridDim.x;
       }
       if ((pass == 1 || a.R <= (int)blockDim.x) && u0 < u1 && mine > 0 && u0 >= pre && u0 < pre + mine) {
         const int64_t item = (u0 - pre) / q.tiles;
         const int hk = (int)(item / q.blocks);
-        *sh = Range{u0, u1, pre, pre + item * q.tiles, pre + (item + 1) * q.tiles, r, hk,
-                    (int)(item - (int64_t)hk * q.blocks), 0, q};
+        *sh = Range{u0, u1, pre, pre + item * q.tiles, pre + (item + 1) * q.tiles, all, r, hk,
+                    (int)(item - (int64_t)hk * q.blocks), -1, -1, q};
         reinterpret_cast<Range*>(a.ws)[blockIdx.x] = *sh;
       }
     }
     if (a.R <= (int)blockDim.x) break;
-    total = run;
-    u0 = total * blockIdx.x / gridDim.x;
-    u1 = total * (blockIdx.x + 1) / gridDim.x;
+    all = run;
+    u0 = all * blockIdx.x / gridDim.x;
+    u1 = all * (blockIdx.x + 1) / gridDim.x;
   }
   if (threadIdx.x == 0 && u0 >= u1) {  // nothing to do
     sh->u0 = sh->u1 = u0;
@@ -596,6 +617,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
       }
     }
   }
+  if (threadIdx.x == 0) note_cut(a, range_s);
   __syncthreads();
   if (threadIdx.x == 0 && abort_s && a.status) atomicOr(a.status, TL_TIMED_OUT);
 }
@@ -603,62 +625,61 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 // Joins the pieces of the row blocks that the CTAs' ranges cut: CTA b looks at
 // the cut at the start of range b, and acts if it is the first of its block.  A
 // lane a row, four output columns at a time; the rows and the halves of the
-// columns are dealt over blockIdx.y.
+// columns are dealt over blockIdx.y.  Short chains of loads are what counts:
+// the range, then maxima and sums and the first outputs together.
 template <int HD, int BM, bool BF>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeAttnArgs a) {
   constexpr int RW = BM < 32 ? BM : 32, CW = 32 / RW;  // rows of a warp, column groups it takes at once
-  __shared__ int16_t ids[1024];
-  __shared__ int count;
+  constexpr int N = 4;                                 // pieces at a time
   pdl_wait();
   const Range* ranges = reinterpret_cast<const Range*>(a.ws);
   const int G = gridDim.x, b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p = ranges[b].cut_first, e = ranges[b].cut_last;
+  if (p < 0) return;
   const Range me = ranges[b];
-  if (me.u0 >= me.u1 || me.u0 == me.ua) return;
-  const int64_t ua = me.ua, ub = me.ub;
-  int p = b - 1;
-  while (ranges[p].u0 >= ranges[p].u1) --p;  // (the block's first unit is in an earlier range)
-  if (ranges[p].u0 > ua) return;             // an earlier cut of the block
-  if (warp == 0) {
-    int n = 1;
-    if (lane == 0) ids[0] = (int16_t)p;
-    for (int c = b + lane;; c += 32) {
-      const bool past = c >= G || ranges[c].u0 >= ub;
-      const bool in = !past && ranges[c].u0 < ranges[c].u1;
-      const unsigned bal = __ballot_sync(0xffffffffu, in);
-      if (in) ids[n + __popc(bal & ((1u << lane) - 1u))] = (int16_t)c;
-      n += __popc(bal);
-      if (__any_sync(0xffffffffu, past)) break;
-    }
-    if (lane == 0) count = n;
-  }
-  __syncthreads();
-  const int np = count, grp = a.H / a.Hk;
+  const bool dense = me.total >= G;  // every CTA has units
+  const int grp = a.H / a.Hk;
   const int y = (blockIdx.y >> 1) * RW + lane % RW, rho = me.blk * BM + y;
   if (rho >= me.q.n * grp) return;
   const int node = rho / grp, head = me.hk * grp + rho - node * grp;
   const int64_t row = me.q.row0 + node;
+  auto holds = [&](int c) { return c <= e && (dense || ranges[c].u0 < ranges[c].u1); };
+  float2 ml[N];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      ml[i] = holds(c0 + i) ? piece_of<HD, BM>(a, G, c0 + i, c0 + i == p)->ml[y] : make_float2(-INFINITY, 0.f);
+  };
   float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < np; ++i) m = fmaxf(m, piece_of<HD, BM>(a, G, ids[i], i == 0)->ml[y].x);
-  const float z = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int i = 0; i < np; ++i) {
-    const float2 ml = piece_of<HD, BM>(a, G, ids[i], i == 0)->ml[y];
-    l += ml.y * ex2(ml.x - z);
+  for (int c = p; c <= e; c += N) {
+    load(c);
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mn = fmaxf(mn, ml[i].x);
+    const float z = mn == -INFINITY ? 0.f : mn;
+    l *= ex2(m - z);
+#pragma unroll
+    for (int i = 0; i < N; ++i) l += ml[i].y * ex2(ml[i].x - z);
+    m = mn;
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const float z = m == -INFINITY ? 0.f : m, inv = l > 0.f || l != l ? 1.f / l : 0.f;
   constexpr int half = HD / 8;  // column groups of a half
   for (int c = (blockIdx.y & 1) * half + warp * CW + lane / RW; c < ((int)(blockIdx.y & 1) + 1) * half; c += 8 * CW) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-      const auto* w = piece_of<HD, BM>(a, G, ids[i], i == 0);
-      const float f = ex2(w->ml[y].x - z);
-      const float4 v = w->o[c][y];
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+    for (int c0 = p; c0 <= e; c0 += N) {
+      if (e - p >= N) load(c0);
+      float4 v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = holds(c0 + i) ? piece_of<HD, BM>(a, G, c0 + i, c0 + i == p)->o[c][y] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float f = ex2(ml[i].x - z);
+        o.x += f * v[i].x;
+        o.y += f * v[i].y;
+        o.z += f * v[i].z;
+        o.w += f * v[i].w;
+      }
     }
     o.x *= inv;
     o.y *= inv;
@@ -672,7 +693,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeAttnArgs a) {
     if (a.out16) {
       const float v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) act16_put(a.out16, row, a.H * HD, head * HD + c * 4 + e, v[e], a.split16);
+      for (int i = 0; i < 4; ++i) act16_put(a.out16, row, a.H * HD, head * HD + c * 4 + i, v[i], a.split16);
     }
   }
   if (a.lse && blockIdx.y % 2 == 0 && warp == 0 && lane < RW)

@@ -556,6 +556,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
       }
     }
   }
+  if (threadIdx.x == 0) note_cut(a, range_s);
   tc_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag && a.status) atomicOr(a.status, TL_TIMED_OUT);
