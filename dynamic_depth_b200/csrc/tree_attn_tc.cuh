@@ -16,15 +16,17 @@
 //
 // Two CTAs an SM, each with half of shared memory and TMEM: one streams while
 // the other is between row blocks (the last tile's masks, the output, the next
-// queries: some 25,000 cycles where 25 tiles of 128 positions take 70,000).
-// With one CTA of 128-position tiles and three rings of buffers the same
-// 64 requests x 32 nodes x 4 heads on 4,000 positions took 252-259 us.
+// queries: some 20,000 cycles, where 25 tiles of 128 positions take 70,000).
+// 64 requests x 32 nodes x 4 heads on 4,000 positions of width 128 take 233 us
+// (4.7 TB/s, 580 TFLOP/s); one CTA an SM with 128-position tiles took 252, two
+// threads a row with three S buffers 259, two groups of rows on alternate tiles
+// 374.
 //
 // Warp 0 loads K, warp 2 loads V (each its own ring), warp 1 issues Q K^T, warp
 // 3 issues P V, so no one of them waits for another's turn; warps 4-7: rows.
-// Bound by the cache's bytes up to 128 rows: 64 positions of width 128 are
-// 32 KB (about 1,400 cycles of one SM's share of HBM) against 12 MMAs and 64
-// exponentials a thread (512 cycles of the SM's).
+// Bound by the issue of matrix instructions: each takes about 110 cycles up to
+// N = 128 whatever its size, and a tile of width 128 needs 12 (1,350 cycles; its
+// 32 KB are about 1,400 of one SM's share of HBM, its exponentials 512).
 #pragma once
 
 #include "ptx.cuh"
