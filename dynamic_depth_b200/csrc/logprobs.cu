@@ -21,9 +21,8 @@
 //
 // Per lane S and T are fp32 sums of vocab / (256 * CTAs) terms or so, joined
 // in fp32 trees.  Bound by issue as much as by memory: 1000 rows of 131,072 bf16
-// logits with n = 20 take 60 us (4.4 TB/s; the pass over the row alone 30 us for
-// 592 of them, 5.2 TB/s, 9 instructions an element), the rest is the end of each
-// row.
+// logits with n = 20 take 61 us (4.3 TB/s), without the best 20 53 us (5.0 TB/s);
+// the difference is the end of each row.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

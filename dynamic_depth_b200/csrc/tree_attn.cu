@@ -25,8 +25,8 @@
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.  64 single tokens x 32 heads over 8 key heads, 4,000
-// positions of width 128: 178 us, 5.9 TB/s (90 % of a copy), pages of 16 or 64;
-// 512 such requests of 500 positions: 236 us, 4.5 TB/s (323 us with one CTA of
+// positions of width 128: 177 us, 5.9 TB/s (91 % of a copy), pages of 16 or 64;
+// 512 such requests of 500 positions: 234 us, 4.5 TB/s (323 us with one CTA of
 // eight multiplying warps an SM).
 #include "tree_attn.h"
 

@@ -15,10 +15,10 @@
 // per tile.
 //
 // Two CTAs an SM, each with half of shared memory and TMEM: one streams while
-// the other is between row blocks (the last tile's masks, the output, the next
-// queries: some 20,000 cycles, where 25 tiles of 128 positions take 70,000).
-// 64 requests x 32 nodes x 4 heads on 4,000 positions of width 128 take 233 us
-// (4.7 TB/s, 580 TFLOP/s); one CTA an SM with 128-position tiles took 252, two
+// the other is between row blocks (the next queries, the output: about a tenth
+// of a CTA's time in the case below).
+// 64 requests x 32 nodes x 4 heads on 4,000 positions of width 128 take 230 us
+// (4.7 TB/s, 590 TFLOP/s); one CTA an SM with 128-position tiles took 252, two
 // threads a row with three S buffers 259, two groups of rows on alternate tiles
 // 374.
 //
