@@ -167,6 +167,15 @@ def test_workspace_holds_a_resident_fp16_copy_of_every_block():
 A = 0x1000  # an aligned address that nothing reads: every call here is refused before anything is enqueued
 
 
+def test_plan_batch_row_limits():
+    def plan(n_rows, parents):
+        return _lib.lib().tl_plan_batch(A, A, 2, 16, A, 4, A, 3, A, parents, n_rows, 0, A, A + 128, A, A + 64, A, A, None,
+                                        None, None)
+    assert plan((1 << 30) + 1, None) == _lib.TL_EINVAL
+    assert plan((1 << 31) - 1, None) == _lib.TL_EINVAL
+    assert plan((1 << 20) + 1, A) == _lib.TL_EINVAL
+
+
 def _pool(**kw):
     f = dict(dev_pool=A, n_pages=4, dtype=_lib.TL_F16, n_kv_heads=2, head_dim=64, page_tokens=16)
     f.update(kw)
