@@ -50,6 +50,9 @@ namespace tree {
 constexpr int kWarps = 4;                     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr float kLn2 = 0.6931471805599453f;
+// Limits that keep positions, rows of a key head and mask bits, each rounded up to a tile, within 31 bits.
+constexpr int64_t kMaxLen = (int64_t(1) << 31) - 4096, kMaxRows = int64_t(1) << 30;
+constexpr int kMaxR = 1 << 20, kMaxWords = 1 << 20;
 
 template <int HD>
 struct Cfg {
@@ -162,7 +165,7 @@ template <int KT, int BM>
 __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r) {
   Req q;
   const int c0 = a.cu[r], c1 = a.cu[r + 1], ctx = a.ctx[r];
-  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int64_t cap = min((int64_t)a.max_pages << a.page_shift, kMaxLen);
   q.bad = c0 < 0 || c1 < c0 || c1 > a.n_rows || c1 - c0 > a.max_nodes || ctx < 0 ||
           (int64_t)ctx + a.node0 + (c1 - c0) > cap;
   q.row0 = c0;
@@ -820,11 +823,12 @@ extern "C" int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_k
   if (!kv_pool_ok(pool)) return TL_EINVAL;
   const int64_t width = (int64_t)n_heads * pool->head_dim;
   const int os = out_dtype == TL_F32 ? 4 : 2;
-  if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || n_rows < 0 || max_pages < 1 || max_nodes < 1 ||
+  if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || R > tree::kMaxR || n_rows < 0 || max_pages < 1 || max_nodes < 1 ||
       (out_dtype != TL_F32 && out_dtype != pool->dtype) || (n_rows > 1 && (q_stride < width || out_stride < width)) ||
       (q_stride * 2) % 16 || (out_stride * os) % 16 || (dev_masks != nullptr) != (mask_words > 0) || mask_words < 0 ||
-      (dev_masks && max_nodes > 32 * (int64_t)mask_words) || !(scale >= 0.f) || scale > 3e38f ||
-      (int64_t)max_nodes * (n_heads / pool->n_kv_heads) > 0x7fffffff)
+      mask_words > tree::kMaxWords ||
+      (dev_masks && max_nodes > 32 * (int64_t)mask_words) || !(scale >= 0.f) || scale > 1e38f ||
+      (int64_t)max_nodes * (n_heads / pool->n_kv_heads) > tree::kMaxRows)
     return TL_EINVAL;
   if (R == 0 || n_rows == 0) return TL_OK;
   if (!dev_q || !dev_block_table || !dev_ctx || !dev_cu || !dev_out || !dev_workspace) return TL_EINVAL;

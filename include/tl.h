@@ -644,8 +644,10 @@ int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t rows, int64_
  *   n_rows: rows dev_q and dev_out hold;
  *   max_nodes: the most nodes a request has; with masks <= 32 * mask_words.
  *     A request with more nodes, with a negative length, with rows past n_rows
- *     or with positions past max_pages is left out (TL_BAD_LENGTH);
- *   scale: 0 means 1 / sqrt(head_dim);
+ *     or with positions past max_pages or 2^31 - 4096 is left out
+ *     (TL_BAD_LENGTH);
+ *   scale: 0 means 1 / sqrt(head_dim); at most 1e38;
+ *   R <= 2^20, mask_words <= 2^20, max_nodes * n_heads / n_kv_heads <= 2^30;
  *   dev_workspace: tl_tree_attention_workspace() bytes, 256-byte aligned; its
  *     contents need no preparation and mean nothing afterwards, but calls that
  *     may run at the same time need one each. */

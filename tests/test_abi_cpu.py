@@ -247,6 +247,17 @@ def test_tree_attention_refusals(kw):
     assert st == _lib.TL_EINVAL
 
 
+@pytest.mark.parametrize("kw", [dict(R=(1 << 20) + 1), dict(words=(1 << 20) + 1), dict(nodes=(1 << 30) + 1, masks=None),
+                                dict(nodes=(1 << 31) - 1, masks=None), dict(scale=2e38)])
+def test_tree_attention_size_limits(kw):
+    a = dict(R=2, nodes=8, masks=A, words=1, scale=0.0)
+    a.update(kw)
+    words = a["words"] if a["masks"] else 0
+    st = _lib.lib().tl_tree_attention(A, 128, _pool(), A, 4, A, A, a["R"], 3, 2, a["nodes"], a["masks"], words,
+                                      a["scale"], A, _lib.TL_F16, 128, A, A, 1 << 62, None, None)
+    assert st == _lib.TL_EINVAL
+
+
 def test_rope_table_refusals():
     lib = _lib.lib()
     for table, length, hd, base in ((None, 4, 64, 1e4), (A + 4, 4, 64, 1e4), (A, 0, 64, 1e4), (A, 4, 63, 1e4),

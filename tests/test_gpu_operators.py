@@ -489,6 +489,22 @@ def test_tree_bad_pages_and_lengths():
     assert st == _lib.TL_BAD_LENGTH and (o[3:5] == 5.0).all() and torch.equal(o[5:], keep[5:])
 
 
+@pytest.mark.parametrize("nodes", [2, 40])
+def test_tree_lengths_near_31_bits_are_left_out(nodes):
+    # a table can repeat pages, so it can hold more positions than an index of 31 bits: the request is left out
+    page, max_pages = 1024, 1 << 21
+    pool = torch.zeros(1, 2, 1, page, 128, dtype=F16, device="cuda")
+    table = torch.zeros(1, max_pages, dtype=torch.int32, device="cuda")
+    q = torch.ones(nodes, 1, 128, dtype=F16, device="cuda")
+    cu = torch.tensor([0, nodes], dtype=torch.int32, device="cuda")
+    for ctx in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 4095 - nodes):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 5.0)
+        T.tree_attention(q, pool, table, torch.tensor([ctx], dtype=torch.int32, device="cuda"), cu, nodes, out=out,
+                         status=st)
+        assert int(st) == _lib.TL_BAD_LENGTH and (out == 5.0).all()
+
+
 def test_tree_far_pages():
     # a pool whose last pages lie past 2^31 elements
     page, hd, Hk = 64, 128, 8
