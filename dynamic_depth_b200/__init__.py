@@ -176,7 +176,7 @@ class LoopedLM:
 
     def score(self, lane: int, tokens, L: int, n_top: int = 0, share_from: int = -1, shared_tokens: int = 0):
         """Prefill a lane and score its tokens: a TokenLogprobs of device tensors, one row per position computed
-        (the last position has no target)."""
+        (the last position has no target), written on the context's stream."""
         from .ops import TokenLogprobs
         tok = np.ascontiguousarray(tokens, dtype=np.int32)
         torch, T = self.torch, len(tok)

@@ -234,7 +234,7 @@ extern "C" int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t r
   if (dtype != TL_F32 && dtype != TL_F16 && dtype != TL_BF16) return TL_EINVAL;
   const int es = dtype == TL_F32 ? 4 : 2;
   const int64_t width = ((int64_t)n_heads + 2 * pool->n_kv_heads) * pool->head_dim;
-  if (rows < 0 || n_heads < 1 || n_heads % pool->n_kv_heads || (rows > 1 && row_stride < width) ||
+  if (rows < 0 || rows > (int64_t(1) << 40) || n_heads < 1 || n_heads % pool->n_kv_heads || (rows > 1 && row_stride < width) ||
       (row_stride * es) % 16 || length < 1 || (dev_q_gain == nullptr) != (dev_k_gain == nullptr) || !(eps >= 0.f))
     return TL_EINVAL;
   if (rows == 0) return TL_OK;

@@ -32,6 +32,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "host_util.h"
 #include "packed.cuh"
@@ -730,7 +732,7 @@ static int launch(K kern, int ctas, int threads, int smem, const TreeAttnArgs& a
                          {HD * 2, cols * 2, (uint64_t)p.n_kv_heads * p.page_tokens * HD * 2}, {cols, pr, HD / cols, 2},
                          sw));
   }
-  static uint64_t set = 0;  // per kernel: one bit per device
+  static std::atomic<uint64_t> set{0};  // per kernel: one bit per device
   int dev = 0;
   TL_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !(set >> dev & 1)) {

@@ -126,7 +126,7 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
             _flat(free_head, i32, 1, "free_head", dev), _flat(parents, i32, n_rows, "parents", dev), n_rows,
             mask_words)
     st = _flat(status, i32, 1, "status", dev)
-    _need(0 <= mask_words <= 8 and n_rows >= 0, "mask_words 0 .. 8 and n_rows of 0 or more are wanted")
+    _need(0 <= mask_words <= 8 and 0 <= n_rows < 1 << 31, "mask_words 0 .. 8 and n_rows of 0 or more are wanted")
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens, n_rows, parents,
@@ -206,8 +206,8 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     themselves).  out: a given tensor's type (the pool's or fp32), else the pool's.  Returns out, or (out, lse)."""
     p = _pool(pool)
     dev, hd = pool.device, p.head_dim
-    _need(q.dim() == 3 and q.dtype == pool.dtype and q.shape[2] == hd and q.stride(2) == 1 and q.stride(1) == hd
-          and q.device == dev, "q: [rows, heads, width] of the pool's type, heads adjacent")
+    _need(q.dim() == 3 and q.dtype == pool.dtype and q.shape[2] == hd and q.stride(2) == 1
+          and (q.stride(1) == hd or q.shape[1] == 1) and q.device == dev, "q: [rows, heads, width] of the pool's type, heads adjacent")
     rows, H = q.shape[0], q.shape[1]
     R = ctx_lens.numel()
     i32 = torch.int32
@@ -217,7 +217,7 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     cp, up = _flat(ctx_lens, i32, R, "ctx_lens", dev), _flat(cu, i32, R + 1, "cu", dev)
     words = 0
     if masks is not None:
-        _need(masks.dim() == 2 and masks.shape[0] == rows, "masks: int32 [rows, words] is wanted")
+        _need(masks.dim() == 2 and masks.shape[0] == rows and masks.shape[1] > 0, "masks: int32 [rows, words] is wanted")
         words = masks.shape[1]
     mp = _flat(masks, i32, rows * words, "masks", dev)
     st = _flat(status, i32, 1, "status", dev)
@@ -228,8 +228,8 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     if out is None:
         out = _alloc((rows, H, hd), (H * hd, hd, 1), q.dtype)
     else:
-        _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1 and out.stride(1) == hd
-              and out.device == dev, "out: the shape of q, heads adjacent")
+        _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1
+              and (out.stride(1) == hd or H == 1) and out.device == dev, "out: the shape of q, heads adjacent")
     lse = _alloc((rows, H), (H, 1), torch.float32) if return_lse else None
     if workspace is None:
         n = _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev.index)

@@ -614,10 +614,13 @@ int tl_rope_table(float* dev_table, int32_t length, int32_t head_dim, double bas
  *   dev_q_gain / dev_k_gain: fp32 [head_dim], both or neither;
  *   dev_table: tl_rope_table's layout, `length` positions; dev_positions int32;
  *   dev_slots: int64, as from tl_plan_batch; -1: the row's keys and values are
- *     not stored.  Two rows with the same slot leave either's values there;
+ *     not stored.  Two rows with the same slot leave a mixture of their values
+ *     there;
  *   dev_q_out: the pool's dtype [rows][n_heads][head_dim], 16-byte aligned.
  * A row whose position is outside the table is left out (TL_BAD_POSITION); a
- * slot outside the pool is not written (TL_BAD_SLOT).  rows may be 0.
+ * slot outside the pool is not written (TL_BAD_SLOT).  The sum of squares is
+ * fp32: heads with elements past 1e18 may come out as zeros.  dev_q_out must not
+ * overlap dev_qkv.  rows may be 0, at most 2^40.
  * n_heads a multiple of n_kv_heads. */
 int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t rows, int64_t row_stride, int32_t n_heads,
                         const float* dev_q_gain, const float* dev_k_gain, float eps, const float* dev_table,

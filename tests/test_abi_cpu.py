@@ -281,3 +281,6 @@ def test_operator_wrappers_refuse_host_tensors_and_shapes():
         T.norm_rope_append(torch.zeros(2, 100), 1, pool, z.long(), z, torch.zeros(4, 32, 2))
     with pytest.raises(ValueError):
         T.tree_attention(torch.zeros(2, 1, 64), pool, torch.zeros(1, 4, dtype=torch.int32), z[:1], z, 1)
+    with pytest.raises(ValueError, match="masks"):  # no words is not the same as no masks
+        T.tree_attention(torch.zeros(2, 1, 64, dtype=torch.float16), pool, torch.zeros(1, 4, dtype=torch.int32), z[:1], z,
+                         1, masks=torch.zeros(2, 0, dtype=torch.int32))

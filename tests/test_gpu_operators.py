@@ -557,6 +557,37 @@ def test_tree_graph_replay_and_other_stream():
     assert torch.equal(outs[0], run_tree(c)[0])
 
 
+def test_tree_calls_on_two_streams_at_once():
+    # different widths and row counts share the SMs, their shared memory and their tensor memory
+    cases = [tree_case([900, 2100, 64], [40, 33, 9], 4, 4, 128, BF16, 64, seed=12),
+             tree_case([1500, 700], [60, 64], 8, 2, 64, BF16, 16, seed=13)]
+    want = [run_tree(c)[0] for c in cases]
+    dev = [{k: torch.from_numpy(c[k]).cuda() for k in ("table", "ctx", "cu")} for c in cases]
+    masks = [mask_tensor(c["see"]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(T.tree_attention(c["q"], c["pool"], dev[i]["table"], dev[i]["ctx"], dev[i]["cu"], c["most"],
+                                                masks=masks[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, want[i])
+
+
+def test_tree_one_head_of_a_wider_projection():
+    # q and out of one head, cut from rows of more: the heads' stride means nothing
+    c = tree_case([75], [3], 1, 1, 64, F16, 16, seed=14)
+    want, _, _ = run_tree(c)
+    wide = torch.zeros(3, 64 * 5, dtype=F16, device="cuda")
+    wide[:, 64:128] = c["q"][:, 0]
+    c["q"] = wide[:, 64:128].unsqueeze(1)
+    assert torch.equal(run_tree(c)[0], want)
+
+
 # ------------------------------------------------------------------- together --
 def test_a_serving_step():
     """Plan, append and attention of two steps: a prompt, then a tree of drafts, against attention over the same keys
