@@ -18,21 +18,23 @@
 // warps multiply, split over the block's 16-row parts and, where those are
 // fewer than four, over parts of the tile's keys.  Every warp keeps its own
 // running state over the keys it sees; the states of a row block meet once per
-// block, in shared memory.  A page's part of a tile, keys and values of one
+// block, in shared memory, where each warp joins and writes a share of the
+// columns.  A page's part of a tile, keys and values of one
 // head, is one four-dimensional TMA box: with one box per 64 columns of keys or
 // values, pages of 16 positions streamed at 4.4 TB/s where pages of 64 reached
 // 5.6.
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.  64 single tokens x 32 heads over 8 key heads, 4,000
-// positions of width 128: 177 us, 5.9 TB/s (91 % of a copy), pages of 16 or 64;
-// 512 such requests of 500 positions: 234 us, 4.5 TB/s (323 us with one CTA of
+// positions of width 128: 175 us, 6.0 TB/s (92 % of a copy), pages of 16 or 64;
+// 512 such requests of 500 positions: 212 us, 5.0 TB/s (323 us with one CTA of
 // eight multiplying warps an SM).
 #include "tree_attn.h"
 
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -65,7 +67,7 @@ struct Cfg {
   static constexpr int STAGE = 2 * KT * HD * 2;     // K and V of a tile
   static constexpr int STAGES = HD == 32 ? 4 : 2;
   static constexpr int SLOT = (HD / 2 + 4) * 32;    // floats of one warp's state: output, 2 maxima, 2 sums
-  static constexpr int MERGE = 2 * SLOT * 4;
+  static constexpr int MERGE = kWarps * SLOT * 4;
   static constexpr int SMEM = 1024 + STAGES * STAGE + MERGE + 256;
   static_assert(SMEM + 1024 <= 113 * 1024, "two CTAs per SM");
 };
@@ -332,7 +334,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
   extern __shared__ __align__(1024) uint8_t smem_ta[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_ta) + 1023) & ~uintptr_t(1023));
   float* merge = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(merge + 2 * C::SLOT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(merge + kWarps * C::SLOT);
   uint64_t* empty = full + C::STAGES;
   volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(empty + C::STAGES);  // [STAGES] boxes that landed
   __shared__ int32_t abort_s;
@@ -442,38 +444,51 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           // -------------------------------------------------- what each row sees
           const bool mask = landed != all_boxes || key0 + KW > q.ctx;
           bool odd_v = false;  // values of the tree hold NaN or infinity
+          // Values of positions that nobody sees may be anything, and 0 * NaN is not 0: they leave the matrix product as
+          // zeros, by masks of the lane's two keys of each 8 (64 ragged single tokens: 123 us, 135 with zeros written to the tile).
+          uint32_t vm[NT / 2][2];
           if (mask) {
+            constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
+            uint32_t tm[NT / 2][2];  // the tree's among them
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
+              uint32_t v = 0, t2 = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kt = wn * KW + i * 8 + c0 + (e & 1), pos = t * KT + kt, j = pos - q.ctx;
-                bool see = pos < q.len && (landed >> (kt / PR) & 1u);
-                if (see && j >= 0) {
-                  const int nd = node[e >> 1];
-                  see = nd >= 0 && (a.masks ? j < 32 * a.words &&
-                                                  (__ldg(a.masks + row[e >> 1] * a.words + (j >> 5)) >> (j & 31) & 1u)
-                                            : j <= nd + a.node0);
+              for (int h = 0; h < 2; ++h) {
+                const int kt = wn * KW + i * 8 + c0 + h, pos = t * KT + kt, j = pos - q.ctx;
+                const bool there = pos < q.len && (landed >> (kt >> pshift) & 1u);
+                v |= there ? 0xffffu << 16 * h : 0u;
+                t2 |= there && j >= 0 ? 0xffffu << 16 * h : 0u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  bool see = there;
+                  if (see && j >= 0) {
+                    const int nd = node[e];
+                    see = nd >= 0 && (a.masks ? j < 32 * a.words &&
+                                                    (__ldg(a.masks + row[e] * a.words + (j >> 5)) >> (j & 31) & 1u)
+                                              : j <= nd + a.node0);
+                  }
+                  if (!see) S[i][2 * e + h] = -INFINITY;
                 }
-                if (!see) S[i][e] = -INFINITY;
               }
-            // values of positions that nobody sees may be anything: 0 * NaN is not 0
-            const bool scan = q.len > q.ctx + 1 || a.masks;
-            for (int i = lane; i < KW * (HD / 8); i += 32) {
-              const int y = wn * KW + i / (HD / 8), pos = t * KT + y;
-              uint4* p = reinterpret_cast<uint4*>(sv + chunk_at(y, i % (HD / 8)));
-              if (pos >= q.len || !(landed >> (y / PR) & 1u)) {
-                *p = make_uint4(0, 0, 0, 0);
-              } else if (scan && pos >= q.ctx) {
-                constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
-                const uint4 w = *p;
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd_v |= (u[e] & X) == X || (u[e] >> 16 & X) == X;
-              }
+              vm[i / 2][i & 1] = v;
+              tm[i / 2][i & 1] = t2;
             }
-            odd_v = __any_sync(0xffffffffu, odd_v);  // orders the zeros before the reads below, too
-            __syncwarp();
+            if ((q.len > q.ctx + 1 || a.masks) && key0 + KW > q.ctx) {
+#pragma unroll
+              for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+                for (int d = 0; d < HD / 16; ++d) {
+                  uint32_t b[4];
+                  ldsm4t(va + v_row[j] + (d * 2 / (C::COLS / 8)) * col_bytes + ((d * 2 % (C::COLS / 8) * 16) ^ v_col), b);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = b[e] & tm[j][e & 1];
+                    odd_v |= (w & X) == X || (w >> 16 & X) == X;
+                  }
+                }
+              odd_v = __any_sync(0xffffffffu, odd_v);
+            }
           }
           // -------------------------------------------------- running maximum and sum
           float mx[2] = {-INFINITY, -INFINITY};
@@ -505,10 +520,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
               l[e >> 1] += S[i][e];
             }
           // -------------------------------------------------- O += P V
-          if (!odd_v) {
+          // one rounding of each probability to the values' type (the matrix instruction takes one type)
+          auto pv = [&](auto masked) {
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) {
-              // one rounding of each probability to the values' type (the matrix instruction takes one type)
               const uint32_t p[4] = {pack2<BF>(S[2 * j][0], S[2 * j][1]), pack2<BF>(S[2 * j][2], S[2 * j][3]),
                                      pack2<BF>(S[2 * j + 1][0], S[2 * j + 1][1]),
                                      pack2<BF>(S[2 * j + 1][2], S[2 * j + 1][3])};
@@ -516,10 +531,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
               for (int d = 0; d < HD / 16; ++d) {
                 uint32_t b[4];
                 ldsm4t(va + v_row[j] + (d * 2 / (C::COLS / 8)) * col_bytes + ((d * 2 % (C::COLS / 8) * 16) ^ v_col), b);
+                if constexpr (masked.value) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) b[e] &= vm[j][e & 1];
+                }
                 mma16816<BF>(O[2 * d], p, b[0], b[1]);
                 mma16816<BF>(O[2 * d + 1], p, b[2], b[3]);
               }
             }
+          };
+          if (!mask) {
+            pv(std::false_type{});
+          } else if (!odd_v) {
+            pv(std::true_type{});
           } else {
             // a value that some row does not see is not finite: products by hand, where the row sees the key
             float pl[NT * 4];
@@ -541,71 +565,87 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
               }
             }
           }
-          if (mask) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the stage's next copy
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
         }
 
         // ---------------------------------------- the states of a row block meet
+        // The WN warps of 16 rows put their states down; each then joins its share of the columns and writes it.
+        constexpr int ND = HD / 8 / WN;  // groups of 8 columns of a warp's share
 #pragma unroll
-        for (int half = WN / 2; half >= 1; half >>= 1) {
-          if (wn >= half && wn < 2 * half) {
-            float* b = merge + (wm * half + wn - half) * C::SLOT + lane;
-#pragma unroll
-            for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) b[(d * 4 + e) * 32] = O[d][e];
-            b[(HD / 2) * 32] = m[0];
-            b[(HD / 2 + 1) * 32] = m[1];
-            b[(HD / 2 + 2) * 32] = l[0];
-            b[(HD / 2 + 3) * 32] = l[1];
-          }
-          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-          if (wn < half) {
-            const float* b = merge + (wm * half + wn) * C::SLOT + lane;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float m2 = b[(HD / 2 + i) * 32], mn = fmaxf(m[i], m2);
-              const float z = mn == -INFINITY ? 0.f : mn;
-              const float x = ex2(m[i] - z), y = ex2(m2 - z);
-              l[i] = l[i] * x + b[(HD / 2 + 2 + i) * 32] * y;
-              m[i] = mn;
-              // a state that saw nothing adds nothing, whatever the other holds
-#pragma unroll
-              for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  O[d][2 * i + e] = O[d][2 * i + e] * x + b[(d * 4 + 2 * i + e) * 32] * y;
-            }
-          }
-          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        for (int i = 0; i < 2; ++i) {
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         }
-        if (wn == 0 && ok) {
+        float X[ND][4];
+        if constexpr (WN == 1) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[d][e] = O[d][e];
+        } else {
+          float* b = merge + warp * C::SLOT + lane;
+#pragma unroll
+          for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[(d * 4 + e) * 32] = O[d][e];
+          b[(HD / 2) * 32] = m[0];
+          b[(HD / 2 + 1) * 32] = m[1];
+          b[(HD / 2 + 2) * 32] = l[0];
+          b[(HD / 2 + 3) * 32] = l[1];
+          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+          float f[WN][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            float mn = -INFINITY, ln = 0.f;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) {
+              f[w][i] = merge[(wm + w * WM) * C::SLOT + (HD / 2 + i) * 32 + lane];
+              mn = fmaxf(mn, f[w][i]);
+            }
+            const float z = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) {
+              f[w][i] = ex2(f[w][i] - z);  // a state that saw nothing adds nothing
+              ln = fmaf(merge[(wm + w * WM) * C::SLOT + (HD / 2 + 2 + i) * 32 + lane], f[w][i], ln);
+            }
+            m[i] = mn;
+            l[i] = ln;
           }
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = 0.f;
+#pragma unroll
+              for (int w = 0; w < WN; ++w)
+                x = fmaf(merge[(wm + w * WM) * C::SLOT + ((wn * ND + d) * 4 + e) * 32 + lane], f[w][e >> 1], x);
+              X[d][e] = x;
+            }
+          asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // read before the next block's states
+        }
+        if (ok) {
           const bool whole = s.t0 == 0 && s.t1 == q.tiles;
+          const int col0 = wn * ND * 8 + c0;
           if (whole) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (node[i] < 0) continue;
               const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
-              const int64_t o = row[i] * a.out_stride + (int64_t)head[i] * HD + c0;
+              const int64_t o = row[i] * a.out_stride + (int64_t)head[i] * HD + col0;
 #pragma unroll
-              for (int d = 0; d < HD / 8; ++d) {
-                const float x = O[d][2 * i] * inv, y = O[d][2 * i + 1] * inv;
+              for (int d = 0; d < ND; ++d) {
+                const float x = X[d][2 * i] * inv, y = X[d][2 * i + 1] * inv;
                 if (a.out_f32)
                   *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + d * 8) = make_float2(x, y);
                 else
                   *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + d * 8) = pack2<BF>(x, y);
                 if (a.out16) {
-                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + c0, x, a.split16);
-                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + c0 + 1, y, a.split16);
+                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + col0, x, a.split16);
+                  act16_put(a.out16, row[i], a.H * HD, head[i] * HD + d * 8 + col0 + 1, y, a.split16);
                 }
               }
-              if (a.lse && (lane & 3) == 0)
+              if (a.lse && wn == 0 && (lane & 3) == 0)
                 a.lse[row[i] * a.H + head[i]] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
             }
           } else {
@@ -615,10 +655,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int y = wm * 16 + r0 + 8 * i;
-              if ((lane & 3) == 0) w->ml[y] = make_float2(m[i], l[i]);
+              if (wn == 0 && (lane & 3) == 0) w->ml[y] = make_float2(m[i], l[i]);
 #pragma unroll
-              for (int d = 0; d < HD / 8; ++d)
-                reinterpret_cast<float2*>(&w->o[d * 2 + c0 / 4][y])[c0 / 2 & 1] = make_float2(O[d][2 * i], O[d][2 * i + 1]);
+              for (int d = 0; d < ND; ++d)
+                reinterpret_cast<float2*>(&w->o[(wn * ND + d) * 2 + c0 / 4][y])[c0 / 2 & 1] =
+                    make_float2(X[d][2 * i], X[d][2 * i + 1]);
             }
           }
         }
