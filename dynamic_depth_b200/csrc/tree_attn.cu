@@ -26,8 +26,8 @@
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.  64 single tokens x 32 heads over 8 key heads, 4,000
-// positions of width 128: 175 us, 6.0 TB/s (92 % of a copy), pages of 16 or 64;
-// 512 such requests of 500 positions: 212 us, 5.0 TB/s (323 us with one CTA of
+// positions of width 128: 171 us, 6.1 TB/s (94 % of a copy), pages of 16 or 64;
+// 512 such requests of 500 positions: 195 us, 5.4 TB/s (323 us with one CTA of
 // eight multiplying warps an SM).
 #include "tree_attn.h"
 
@@ -179,6 +179,26 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r) {
   q.tiles = q.len > 0 ? (q.len + KT - 1) / KT : 1;
   q.blocks = (int)(((int64_t)q.n * (a.H / a.Hk) + BM - 1) / BM);
   return q;
+}
+
+// The n lowest bits.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+// Bits of the 32 positions from p0 on that a row sees.
+__device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q, int64_t row, int node, int p0) {
+  const int j0 = p0 - q.ctx;  // node index of the first position
+  uint32_t v = low_bits(-j0);      // the context
+  if (j0 > -32) {
+    if (a.masks) {
+      const uint32_t* w = a.masks + row * a.words;
+      auto word = [&](int i) { return i >= 0 && i < a.words ? __ldg(w + i) : 0u; };
+      v |= j0 >= 0 ? __funnelshift_r(word(j0 >> 5), word((j0 >> 5) + 1), j0 & 31) : word(0) << -j0;
+    } else {
+      v |= low_bits(node + a.node0 + 1 - j0) & ~low_bits(-j0);
+    }
+  }
+  return v & low_bits(q.len - p0);
 }
 
 // A stretch of one row block's key tiles within a CTA's range.
@@ -445,34 +465,32 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           const bool mask = landed != all_boxes || key0 + KW > q.ctx;
           bool odd_v = false;  // values of the tree hold NaN or infinity
           // Values of positions that nobody sees may be anything, and 0 * NaN is not 0: they leave the matrix product as
-          // zeros, by masks of the lane's two keys of each 8 (64 ragged single tokens: 123 us, 135 with zeros written to the tile).
+          // zeros, by masks of the lane's two keys of each 8 (64 ragged single tokens: 123 us then,
+          // 135 with zeros written to the tile).
           uint32_t vm[NT / 2][2];
           if (mask) {
             constexpr uint32_t X = BF ? 0x7f80u : 0x7c00u;
             uint32_t tm[NT / 2][2];  // the tree's among them
+            uint32_t see[2], there = 0, tree = 0;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              uint32_t v = 0, t2 = 0;
+              // Of 32 positions, those that the rows see, that there are, and the tree's, as words: tested one by one
+              // they made a block's last tile cost as much as two (64 ragged single tokens 123 us, 116 so).
+              if (i % 4 == 0) {
+                const int p0 = key0 + i * 8;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int kt = wn * KW + i * 8 + c0 + h, pos = t * KT + kt, j = pos - q.ctx;
-                const bool there = pos < q.len && (landed >> (kt >> pshift) & 1u);
-                v |= there ? 0xffffu << 16 * h : 0u;
-                t2 |= there && j >= 0 ? 0xffffu << 16 * h : 0u;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  bool see = there;
-                  if (see && j >= 0) {
-                    const int nd = node[e];
-                    see = nd >= 0 && (a.masks ? j < 32 * a.words &&
-                                                    (__ldg(a.masks + row[e] * a.words + (j >> 5)) >> (j & 31) & 1u)
-                                              : j <= nd + a.node0);
-                  }
-                  if (!see) S[i][2 * e + h] = -INFINITY;
-                }
+                for (int e = 0; e < 2; ++e) see[e] = row_sees(a, q, row[e], node[e], p0);
+                there = low_bits(q.len - p0);
+                tree = there & ~low_bits(q.ctx - p0);
               }
-              vm[i / 2][i & 1] = v;
-              tm[i / 2][i & 1] = t2;
+              const int at = i % 4 * 8 + c0;
+              const uint32_t box = landed >> ((wn * KW + i * 8) >> pshift) & 1u ? 3u : 0u;
+              const uint32_t v = there >> at & box, w = tree >> at & box;
+              vm[i / 2][i & 1] = (v & 1u) * 0xffffu | (v >> 1) * 0xffff0000u;
+              tm[i / 2][i & 1] = (w & 1u) * 0xffffu | (w >> 1) * 0xffff0000u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!(see[e >> 1] >> at & box & (e & 1 ? 2u : 1u))) S[i][e] = -INFINITY;
             }
             if ((q.len > q.ctx + 1 || a.masks) && key0 + KW > q.ctx) {
 #pragma unroll
@@ -866,7 +884,8 @@ extern "C" int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_k
   if (!kv_pool_ok(pool)) return TL_EINVAL;
   const int64_t width = (int64_t)n_heads * pool->head_dim;
   const int os = out_dtype == TL_F32 ? 4 : 2;
-  if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || R > tree::kMaxR || n_rows < 0 || max_pages < 1 || max_nodes < 1 ||
+  if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || R > tree::kMaxR || n_rows < 0 || max_pages < 1 ||
+      max_nodes < 1 ||
       (out_dtype != TL_F32 && out_dtype != pool->dtype) || (n_rows > 1 && (q_stride < width || out_stride < width)) ||
       (q_stride * 2) % 16 || (out_stride * os) % 16 || (dev_masks != nullptr) != (mask_words > 0) || mask_words < 0 ||
       mask_words > tree::kMaxWords ||

@@ -182,23 +182,6 @@ __device__ __forceinline__ void produce_half(const TreeAttnArgs& a, const CUtens
   }
 }
 
-// Bits of the 32 positions from p0 on that a row sees.
-__device__ __forceinline__ uint32_t row_sees(const TreeAttnArgs& a, const Req& q, int64_t row, int node, int p0) {
-  auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-  const int j0 = p0 - q.ctx;  // node index of the first position
-  uint32_t v = low(-j0);      // the context
-  if (j0 > -32) {
-    if (a.masks) {
-      const uint32_t* w = a.masks + row * a.words;
-      auto word = [&](int i) { return i >= 0 && i < a.words ? __ldg(w + i) : 0u; };
-      v |= j0 >= 0 ? __funnelshift_r(word(j0 >> 5), word((j0 >> 5) + 1), j0 & 31) : word(0) << -j0;
-    } else {
-      v |= low(node + a.node0 + 1 - j0) & ~low(-j0);
-    }
-  }
-  return v & low(q.len - p0);
-}
-
 // Sums p * v of the values of 64 positions that are not finite, over the positions with a probability.
 template <int HD, bool BF>
 __device__ __noinline__ void add_odd(const float* p, const uint8_t* vt, float* add) {
