@@ -26,7 +26,7 @@
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.  64 single tokens x 32 heads over 8 key heads, 4,000
-// positions of width 128: 171 us, 6.1 TB/s (94 % of a copy), pages of 16 or 64;
+// positions of width 128: 174 us, 6.0 TB/s (92 % of a copy), pages of 16 or 64;
 // 512 such requests of 500 positions: 195 us, 5.4 TB/s (323 us with one CTA of
 // eight multiplying warps an SM).
 #include "tree_attn.h"
@@ -81,7 +81,6 @@ struct Req {
 // for the joining kernel.
 struct Range {
   int64_t u0, u1;   // units of this CTA
-  int64_t base;     // first unit of the request that holds u0
   int64_t ua, ub;   // units of the row block that holds u0
   int64_t total;    // units in all
   int32_t r, hk, blk;
@@ -207,27 +206,27 @@ struct Seg {
   int32_t r, hk, blk, t0, t1;
 };
 
+// The stretches of a CTA's range, one after another.
 template <int KT, int BM>
 struct Walk {
-  int64_t u, u1, base;
-  int32_t r;
-  Req q;
-  __device__ __forceinline__ bool next(const TreeAttnArgs& a, Seg& s) {
+  int64_t u, u1;  // units given out, and the range's end
+  Seg s;          // the last one given out; t1 < 0: the first is still to come
+  __device__ __forceinline__ explicit Walk(const Range& g)
+      : u(g.u0), u1(g.u1), s{g.q, g.r, g.hk, g.blk, (int32_t)(g.u0 - g.ua), -1} {}
+  __device__ __forceinline__ bool next(const TreeAttnArgs& a) {
     if (u >= u1) return false;
-    int64_t units = (int64_t)q.tiles * q.blocks * a.Hk;
-    while (u >= base + units) {
-      base += units;
-      q = request<KT, BM>(a, ++r);
-      units = (int64_t)q.tiles * q.blocks * a.Hk;
+    if (s.t1 >= 0) {
+      s.t0 = 0;
+      if (++s.blk == s.q.blocks) {
+        s.blk = 0;
+        if (++s.hk == a.Hk) {
+          s.hk = 0;
+          do s.q = request<KT, BM>(a, ++s.r);
+          while (s.q.blocks == 0);
+        }
+      }
     }
-    const int64_t o = u - base;
-    const int64_t item = o / q.tiles;
-    s.q = q;
-    s.r = r;
-    s.t0 = (int)(o - item * q.tiles);
-    s.t1 = (int)min((int64_t)q.tiles, s.t0 + (u1 - u));
-    s.hk = (int)(item / q.blocks);
-    s.blk = (int)(item - (int64_t)s.hk * q.blocks);
+    s.t1 = (int)min((int64_t)s.q.tiles, s.t0 + (u1 - u));
     u += s.t1 - s.t0;
     return true;
   }
@@ -272,7 +271,7 @@ __device__ __forceinline__ void find_range(const TreeAttnArgs& a, Range* sh, lon
       if ((pass == 1 || a.R <= (int)blockDim.x) && u0 < u1 && mine > 0 && u0 >= pre && u0 < pre + mine) {
         const int64_t item = (u0 - pre) / q.tiles;
         const int hk = (int)(item / q.blocks);
-        *sh = Range{u0, u1, pre, pre + item * q.tiles, pre + (item + 1) * q.tiles, all, r, hk,
+        *sh = Range{u0, u1, pre + item * q.tiles, pre + (item + 1) * q.tiles, all, r, hk,
                     (int)(item - (int64_t)hk * q.blocks), -1, -1, q};
         reinterpret_cast<Range*>(a.ws)[blockIdx.x] = *sh;
       }
@@ -298,10 +297,10 @@ __device__ __forceinline__ void produce(const TreeAttnArgs& a, const CUtensorMap
                                         volatile int32_t* abort_flag) {
   const int lane = threadIdx.x & 31;
   const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR, box_bytes = C::STAGE / boxes;
-  Seg s;
+  const Seg& s = walk.s;
   int k = 0;
   bool ok = true;
-  while (ok && walk.next(a, s)) {
+  while (ok && walk.next(a)) {
     const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
     auto page_of = [&](int t) {
       const int pos = t * KT + lane * PR;
@@ -375,12 +374,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
   find_range<KT, BM>(a, &range_s, wsum);
   __syncthreads();
   if (range_s.u0 < range_s.u1) {
-    Walk<KT, BM> walk{range_s.u0, range_s.u1, range_s.base, range_s.r, range_s.q};
+    Walk<KT, BM> walk(range_s);
+    const Seg& s = walk.s;
     const int64_t u_first = walk.u;
     const int P = 1 << a.page_shift;
     const int PR = P < KT ? P : KT, boxes = KT / PR;  // positions per box, boxes per tile
     const uint32_t all_boxes = (1u << boxes) - 1u;
-    Seg s;
     int k = 0;  // tiles of this CTA so far
     if (warp == kWarps) {
       produce<C, KT, BM>(a, kvmap, walk, ring, full, empty, info, abort_flag);
@@ -406,7 +405,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
         v_row[j] = row_at(wn * KW + j * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
       }
       bool ok = true;
-      while (walk.next(a, s)) {
+      while (walk.next(a)) {
         const Req& q = s.q;
         const int rows = q.n * G;
         int rho[2], node[2];

@@ -17,8 +17,8 @@
 // Two CTAs an SM, each with half of shared memory and TMEM: one streams while
 // the other is between row blocks (the next queries, the output: about a tenth
 // of a CTA's time in the case below).
-// 64 requests x 32 nodes x 4 heads on 4,000 positions of width 128 take 230 us
-// (4.7 TB/s, 590 TFLOP/s); one CTA an SM with 128-position tiles took 252, two
+// 64 requests x 32 nodes x 4 heads on 4,000 positions of width 128 take 229 us
+// (4.8 TB/s, 590 TFLOP/s); one CTA an SM with 128-position tiles took 252, two
 // threads a row with three S buffers 259, two groups of rows on alternate tiles
 // 374.
 //
@@ -113,6 +113,10 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// 16 bytes to shared memory, zeros where there is nothing to read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 // Barrier 1: the 128 row threads.
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // Whether any row thread says so (all of them call it).
@@ -139,10 +143,10 @@ __device__ __forceinline__ void produce_half(const TreeAttnArgs& a, const CUtens
   constexpr int KT = C::KT;
   const int lane = threadIdx.x & 31;
   const int P = 1 << a.page_shift, PR = P < KT ? P : KT, boxes = KT / PR;
-  Seg s;
+  const Seg& s = walk.s;
   int k = 0;
   bool ok = true;
-  while (ok && walk.next(a, s)) {
+  while (ok && walk.next(a)) {
     const int32_t* table = a.table + (int64_t)s.r * a.max_pages;
     const int64_t head = (int64_t)s.hk + (values ? a.Hk : 0);
     auto page_of = [&](int t) {
@@ -278,9 +282,9 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
   find_range<KT, BM>(a, &range_s, wsum);
   __syncthreads();
   const uint32_t tmem = tmem_s;
-  Walk<KT, BM> walk{range_s.u0, range_s.u1, range_s.base, range_s.r, range_s.q};  // nothing where u0 == u1
+  Walk<KT, BM> walk(range_s);  // nothing where u0 == u1
   const int64_t u_first = walk.u;
-  Seg s;
+  const Seg& s = walk.s;
   int k = 0;  // tiles of this CTA so far
   if (warp < 4) {
     if (warp == 0 || warp == 2) {
@@ -290,7 +294,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
       // ------------------------------------------------------------- S = Q K^T
       constexpr uint32_t idesc = tc_idesc(BF, KT, 0);
       bool ok = true;
-      for (int seg = 0; ok && walk.next(a, s); ++seg) {
+      for (int seg = 0; ok && walk.next(a); ++seg) {
         if (!(ok = mbar_wait_warp(smem_u32(q_full), seg & 1, abort_flag))) break;
         for (int t = s.t0; t < s.t1; ++t, ++k) {
           const int st = k % ST, buf = k % SB;
@@ -315,7 +319,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
       // --------------------------------------------------------------- O += P V
       constexpr uint32_t idesc = tc_idesc(BF, HD, 1);
       bool ok = true;
-      while (ok && walk.next(a, s)) {
+      while (ok && walk.next(a)) {
         for (int t = s.t0; t < s.t1; ++t, ++k) {
           const int st = k % ST, buf = k % SB;
           ok = mbar_wait_warp(smem_u32(&v_full[st]), (k / ST) & 1, abort_flag) &&
@@ -344,10 +348,10 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // the warp's TMEM lanes
       const uint32_t to = tl + SB * KT;
       const int G = a.H / a.Hk;
-      const int PR = min(1 << a.page_shift, KT);
-      const uint32_t all_boxes = (1u << (KT / PR)) - 1u;
+      const int PR = min(1 << a.page_shift, KT), pshift = 31 - __clz(PR);
+      const uint32_t all_boxes = (1u << (KT >> pshift)) - 1u;
       bool ok = true;  // once a wait ran out: no more waits or TMEM, but every barrier of the rows is still met
-      while (walk.next(a, s)) {
+      while (walk.next(a)) {
         const int ctx = s.q.ctx, len = s.q.len;
         const int rho = s.blk * BM + t_row;
         const bool valid = rho < s.q.n * G;
@@ -355,13 +359,19 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
         const int64_t row = s.q.row0 + (valid ? node : 0);
         const bool active = __any_sync(0xffffffffu, valid);
         if (ok) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_stride +
-                                                            (int64_t)head * HD);
+          // the warp's 32 rows, neighbouring lanes at neighbouring 16 bytes, all on their way at once (a thread that
+          // loads its own row spreads each load over 32 lines; 16 lanes x 32 nodes: 88.6 us, 94.5 so, with the walk's
+          // divisions)
+          constexpr int CH = HD / 8, RI = 32 / CH;  // 16-byte chunks of a row, rows of an access
+          const int64_t from = valid ? row * a.q_stride + (int64_t)head * HD : -1;
 #pragma unroll
-          for (int c = 0; c < HD / 8; ++c) {
-            const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(sQ + (c / 8) * (BM * 128) + t_row * 128 + (((c % 8) ^ (t_row & 7)) << 4)) = v;
+          for (int i = 0; i < CH; ++i) {
+            const int y = i * RI + lane / CH, c = lane % CH;
+            const int64_t o = __shfl_sync(0xffffffffu, from, y);
+            cp_async16(smem_u32(sQ) + (c / 8) * (BM * 128) + ((warp & 3) * 32 + y) * 128 + (((c % 8) ^ (y & 7)) << 4),
+                       static_cast<const uint16_t*>(a.q) + (o < 0 ? 0 : o + c * 8), o >= 0);
           }
+          asm volatile("cp.async.wait_all;" ::: "memory");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(q_full));
@@ -394,7 +404,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
             if (mask) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const uint32_t lo = landed >> (32 * c / PR) & 1u, hi = landed >> ((32 * c + 16) / PR) & 1u;
+                const uint32_t lo = landed >> (32 * c >> pshift) & 1u, hi = landed >> (32 * c + 16 >> pshift) & 1u;
                 const uint32_t v = (nodes_here ? see[c] : 0xffffffffu) & ((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sv[32 * c + i] = v >> i & 1u ? sv[32 * c + i] : -INFINITY;
@@ -446,7 +456,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
               return reinterpret_cast<uint4*>(vt + (c / 8) * C::TILE + y * 128 + (((c % 8) ^ (y & 7)) << 4));
             };
             bool mine = false;
-            if (pos >= len || !(landed >> (y / PR) & 1u)) {
+            if (pos >= len || !(landed >> (y >> pshift) & 1u)) {
 #pragma unroll
               for (int c = 0; c < HD / 16; ++c) *chunk(c0 + c) = make_uint4(0, 0, 0, 0);
             } else if (pos >= ctx && (len > ctx + 1 || a.masks)) {
