@@ -43,12 +43,12 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _flat(t, dtype, n, name, device):
-    """A contiguous device vector of n elements (None passes as a null pointer)."""
+def _flat(t, dtype, n, name, dev):
+    """A contiguous vector of n elements on CUDA device `dev` (None passes as a null pointer)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements on {device} is wanted")
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements on cuda:{dev} is wanted")
     return t.data_ptr()
 
 
@@ -57,9 +57,10 @@ def _at(t):
 
 
 # A call costs its wrapper before it costs the GPU anything: streams and outputs come from torch's raw entry points
-# where it has them (0.1 against 3.3 us for the current stream, 0.6 against 2.3 us for an empty tensor).
+# where it has them (0.1 against 3.3 us for the current stream, 0.6 against 2.3 us for an empty tensor), and devices
+# are compared by index.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
-_current = torch.cuda.current_device
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda as _alloc  # (sizes, strides, dtype), on the current device
 except ImportError:
@@ -69,9 +70,9 @@ except ImportError:
 
 def _elsewhere(dev):
     """Whether a call's device is not the current one (it then runs again with that made current)."""
-    i = dev.index
-    _need(i is not None, "the tensors must be on a CUDA device")
-    return i != _current()
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    return dev != _current()
 
 
 def _pool(pool) -> TlKvPool:
@@ -87,7 +88,7 @@ def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
     _need(logits.dim() == 2 and logits.dtype in _DT and (logits.shape[1] <= 1 or logits.stride(1) == 1),
           "logits: [rows, vocab] of fp32, fp16 or bf16 with adjacent columns is wanted")
     rows, vocab = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     f32, i32 = torch.float32, torch.int32
     tp = _flat(targets, i32, rows, "targets", dev)
     if _elsewhere(dev):
@@ -103,7 +104,7 @@ def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
         ids, top = _alloc((rows, n_top), (n_top, 1), i32), _alloc((rows, n_top), (n_top, 1), f32)
     check(lib().tl_token_logprobs(
         logits.data_ptr(), _DT[logits.dtype], rows, vocab, logits.stride(0) if rows > 1 else vocab, tp, n_top,
-        _at(lp), _at(rank), ent.data_ptr(), lse.data_ptr(), _at(ids), _at(top), _raw_stream(dev.index)),
+        _at(lp), _at(rank), ent.data_ptr(), lse.data_ptr(), _at(ids), _at(top), _raw_stream(dev)),
         "tl_token_logprobs")
     return TokenLogprobs(lp, rank, ent, lse, ids, top)
 
@@ -114,9 +115,9 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
     [R, max_pages] (int32) gets the pages granted from free_pages[free_head[0]:].  n_rows: rows of the row outputs
     (at least the sum of fresh; rows past that sum are not written)."""
     R = cached.numel()
-    dev = cached.device
+    dev = cached.get_device()
     _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32
-          and block_table.is_contiguous() and block_table.device == dev,
+          and block_table.is_contiguous() and block_table.get_device() == dev,
           "block_table: a contiguous int32 [R, max_pages] tensor is wanted")
     _need(free_pages.dim() == 1, "free_pages: a vector is wanted")
     i32 = torch.int32
@@ -139,7 +140,7 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
     # an empty tensor has no address; the library wants one where a mask is asked for
     mp = None if masks is None else (masks.data_ptr() or cu.data_ptr())
     check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
-                              slots.data_ptr(), pos.data_ptr(), mp, st, _raw_stream(dev.index)), "tl_plan_batch")
+                              slots.data_ptr(), pos.data_ptr(), mp, st, _raw_stream(dev)), "tl_plan_batch")
     return BatchPlan(cu, lens, granted, head, slots, pos, masks)
 
 
@@ -157,9 +158,9 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
     """Per-head RMSNorm (with gains) and rotation of the queries and keys of qkv [rows, (q | k | v) heads * width],
     keys and values stored at `slots` of the pool; returns the queries [rows, n_heads, width] in the pool's type."""
     p = _pool(pool)
-    dev, rows, hd = pool.device, qkv.shape[0], p.head_dim
+    dev, rows, hd = pool.get_device(), qkv.shape[0], p.head_dim
     _need(qkv.dim() == 2 and qkv.dtype in _DT and qkv.shape[1] == (n_heads + 2 * p.n_kv_heads) * hd
-          and qkv.stride(1) == 1 and qkv.device == dev, "qkv: [rows, (q + 2 kv heads) * width] of the pool's device")
+          and qkv.stride(1) == 1 and qkv.get_device() == dev, "qkv: [rows, (q + 2 kv heads) * width] of the pool's device")
     _need(rope.dim() == 3 and rope.shape[1:] == (hd // 2, 2), "rope: a rope_table of the pool's head width is wanted")
     i32, f32 = torch.int32, torch.float32
     sp = _flat(slots, torch.int64, rows, "slots", dev)
@@ -175,7 +176,7 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
     qp = _flat(q_out, pool.dtype, rows * n_heads * hd, "q_out", dev)
     check(lib().tl_norm_rope_append(qkv.data_ptr(), _DT[qkv.dtype], rows, qkv.stride(0) if rows > 1 else qkv.shape[1],
                                     n_heads, gq, gk, eps, rp, rope.shape[0], pp, sp, C.byref(p), qp, st,
-                                    _raw_stream(dev.index)), "tl_norm_rope_append")
+                                    _raw_stream(dev)), "tl_norm_rope_append")
     return q_out
 
 
@@ -205,14 +206,14 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     first ctx_lens[r] positions and the nodes behind them that their mask words name (None: the earlier nodes and
     themselves).  out: a given tensor's type (the pool's or fp32), else the pool's.  Returns out, or (out, lse)."""
     p = _pool(pool)
-    dev, hd = pool.device, p.head_dim
+    dev, hd = pool.get_device(), p.head_dim
     _need(q.dim() == 3 and q.dtype == pool.dtype and q.shape[2] == hd and q.stride(2) == 1
-          and (q.stride(1) == hd or q.shape[1] == 1) and q.device == dev, "q: [rows, heads, width] of the pool's type, heads adjacent")
+          and (q.stride(1) == hd or q.shape[1] == 1) and q.get_device() == dev, "q: [rows, heads, width] of the pool's type, heads adjacent")
     rows, H = q.shape[0], q.shape[1]
     R = ctx_lens.numel()
     i32 = torch.int32
     _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == i32
-          and block_table.is_contiguous() and block_table.device == dev,
+          and block_table.is_contiguous() and block_table.get_device() == dev,
           "block_table: a contiguous int32 [R, max_pages] tensor is wanted")
     cp, up = _flat(ctx_lens, i32, R, "ctx_lens", dev), _flat(cu, i32, R + 1, "cu", dev)
     words = 0
@@ -229,17 +230,17 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
         out = _alloc((rows, H, hd), (H * hd, hd, 1), q.dtype)
     else:
         _need(out.shape == q.shape and out.dtype in _DT and out.stride(2) == 1
-              and (out.stride(1) == hd or H == 1) and out.device == dev, "out: the shape of q, heads adjacent")
+              and (out.stride(1) == hd or H == 1) and out.get_device() == dev, "out: the shape of q, heads adjacent")
     lse = _alloc((rows, H), (H, 1), torch.float32) if return_lse else None
     if workspace is None:
-        n = _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev.index)
+        n = _workspace_bytes(hd, H, p.n_kv_heads, max_nodes, dev)
         workspace = _alloc((n,), (1,), torch.uint8)
     else:
         n = workspace.numel() * workspace.element_size()
-        _need(workspace.is_contiguous() and workspace.device == dev, "workspace: a tree_attention_workspace is wanted")
+        _need(workspace.is_contiguous() and workspace.get_device() == dev, "workspace: a tree_attention_workspace is wanted")
     check(lib().tl_tree_attention(
         q.data_ptr(), q.stride(0) if rows > 1 else H * hd, C.byref(p), block_table.data_ptr(),
         block_table.shape[1], cp, up, R, rows, H, max_nodes, mp, words, scale, out.data_ptr(), _DT[out.dtype],
-        out.stride(0) if rows > 1 else H * hd, _at(lse), workspace.data_ptr(), n, st, _raw_stream(dev.index)),
+        out.stride(0) if rows > 1 else H * hd, _at(lse), workspace.data_ptr(), n, st, _raw_stream(dev)),
         "tl_tree_attention")
     return (out, lse) if return_lse else out
