@@ -221,8 +221,10 @@ struct Walk {
         s.blk = 0;
         if (++s.hk == a.Hk) {
           s.hk = 0;
-          do s.q = request<KT, BM>(a, ++s.r);
-          while (s.q.blocks == 0);
+          do {
+            if (s.r + 1 >= a.R) return false;  // only if the lengths changed during the call
+            s.q = request<KT, BM>(a, ++s.r);
+          } while (s.q.blocks == 0);
         }
       }
     }
