@@ -58,6 +58,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int64_t kMaxLen = (int64_t(1) << 31) - 4096, kMaxRows = int64_t(1) << 30;
 constexpr int kMaxR = 1 << 20, kMaxWords = 1 << 20;
 
+// How far, in powers of two, the reference of a row lies below the largest score
+// seen: probabilities enter the second product up to 2^kLift times larger, and
+// the sum and the natural-log result follow the same reference.  fp16 loses
+// probabilities below 2^-14 of its 1 digit by digit, and all below 2^-25, while
+// the sum keeps them: relative to the maximum itself, 6,000 keys at 2^-24.3 of
+// the largest came out 3.6 % off.  At 2^7 what is lost is below 2^-32 of the
+// largest, and the tensor-core kernel's probabilities (up to 2^8 past the
+// reference) end at 2^15, inside fp16.  bf16 has fp32's range.
+template <bool BF>
+constexpr float kLift = BF ? 0.f : 7.f;
+
 template <int HD>
 struct Cfg {
   static constexpr int KT = HD == 128 ? 64 : 128;   // key positions per tile
@@ -521,7 +532,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
           for (int i = 0; i < 2; ++i) {
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-            const float mn = fmaxf(m[i], mx[i] * a.scale_log2);
+            const float mn = fmaxf(m[i], mx[i] * a.scale_log2 - kLift<BF>);
             mb[i] = mn == -INFINITY ? 0.f : mn;
             const float corr = ex2(m[i] - mb[i]);  // 0 from -inf
             l[i] *= corr;

@@ -9,10 +9,10 @@
 //   P = exp2(S-m)  one thread a row; 16-bit P replaces S in its TMEM columns
 //   O += P V       tcgen05.mma with P as the TMEM operand A and V (rows of
 //                  keys) as the N-major operand B, accumulating in TMEM
-// The reference m of a row moves only when a tile's maximum passes it by more
-// than 2^8 (P then stays below 256, far inside fp16 and bf16, and sums are
-// fp32), so O is rescaled in TMEM a few times per row block instead of once
-// per tile.
+// The reference m of a row (kLift below a maximum) moves only when a tile's
+// maximum passes the last one by more than 2^8 (P then stays below 2^15 in fp16
+// and 2^8 in bf16, and sums are fp32), so O is rescaled in TMEM a few times per
+// row block instead of once per tile.
 //
 // Two CTAs an SM, each with half of shared memory and TMEM: one streams while
 // the other is between row blocks (the next queries, the output: about a tenth
@@ -415,8 +415,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArg
             for (int i = 4; i < KT; i += 4)
 #pragma unroll
               for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[i + e]);
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-            // the row's reference: the first tile's maximum, and a new one only past 2^8 times it
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2 - kLift<BF>;
+            // the row's reference, from the first tile's maximum, and a new one only past 2^8 times it
             const bool move = mt > (t == s.t0 ? m : m + 8.f);
             const float mn = move ? mt : m, z = mn == -INFINITY ? 0.f : mn;
             if (t > s.t0 && __any_sync(0xffffffffu, move)) {

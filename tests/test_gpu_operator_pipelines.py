@@ -59,7 +59,8 @@ def striped_values(c, seed):
 
 
 def definition(c, scale):
-    """(out, lse, bound on out, bound on lse) in fp64 on the GPU; the bounds are operator_refs.tree_attention's."""
+    """(out, lse, bound on out, bound on lse) in fp64 on the GPU; the bounds are operator_refs.tree_attention's, but
+    for what fp16 probabilities lose: they are held 2^7 times larger, so a denormal one is off by 2^-32 of the largest."""
     rows, H, hd = c["q"].shape
     Hk = c["pool"].shape[2]
     G = H // Hk
@@ -93,7 +94,7 @@ def definition(c, scale):
         rel = (2 * ds + keys * 2.0 ** -23 + 2.0 ** -19).permute(1, 0, 2)[..., None]
         t = (half + rel) * mag + half * o.abs() + 1e-7
         if c["q"].dtype == F16:
-            t = t + (keys * 2.0 ** -25 / z[..., 0]).permute(1, 0, 2)[..., None] * v.abs().amax(0)[None, :, None]
+            t = t + (keys * 2.0 ** -32 / z[..., 0]).permute(1, 0, 2)[..., None] * v.abs().amax(0)[None, :, None]
         ll = (m + torch.log(z))[..., 0]
         lt = ds + keys * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * ll.abs()
         out[a:b], tol[a:b] = o.reshape(n, H, hd), t.reshape(n, H, hd)
@@ -163,3 +164,26 @@ def test_scores_that_climb(hd, dtype, nodes):
         put(c, r, 0, k)
         put(c, r, 1, v)
     check(c, 2)
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("nodes", [1, 40])
+@pytest.mark.parametrize("gap", [24.3, 25.5])
+def test_probabilities_far_below_the_largest_keep_their_share(hd, nodes, gap):
+    """One key of value 0 has 2^gap times the weight of each other, whose values are 1: what is left of the result is
+    their share, which fp16 probabilities relative to the largest would lose (below 2^-25) or double (below 2^-24)."""
+    n_req, ctx = 24, 6000
+    c = tree_case([ctx] * n_req, [nodes] * n_req, 8, 8, hd, F16, 64, seed=hd)
+    c["q"] = torch.ones_like(c["q"])
+    for r in range(n_req):
+        k = torch.zeros(ctx + nodes, 8, hd, device="cuda")
+        k[0] = gap * math.log(2) / math.sqrt(hd)
+        v = torch.ones(ctx + nodes, 8, hd, device="cuda")
+        v[0] = 0
+        put(c, r, 0, k)
+        put(c, r, 1, v)
+    wo, wl, tol, ltol = definition(c, hd ** -0.5)
+    assert float(tol.max()) < 0.02 * float(wo.min())  # the bound sees a fiftieth of their share
+    o, lse, st = run_tree(c)
+    off, loff = float(((o.double() - wo).abs() / tol).max()), float(((lse.double() - wl).abs() / ltol).max())
+    assert st == 0 and off <= 1 and loff <= 1, (off, loff)
