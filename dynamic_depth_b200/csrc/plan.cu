@@ -198,8 +198,9 @@ extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh
                              int32_t* dev_free_head_out, int64_t* dev_slots, int32_t* dev_positions,
                              uint32_t* dev_masks, int32_t* dev_status, void* cuda_stream) {
   if (R < 1 || R > plan::kMaxR || page_tokens < 1 || page_tokens > 4096 || (page_tokens & (page_tokens - 1)) ||
-      max_pages < 1 || n_free < 0 || n_rows < 0 || n_rows > (dev_parents ? plan::kMaxTreeRows : plan::kMaxRows) || mask_words < 0 || mask_words > plan::kMaxWords ||
-      (mask_words > 0) != (dev_masks != nullptr))
+      max_pages < 1 || n_free < 0 || n_rows < 0 || n_rows > (dev_parents ? plan::kMaxTreeRows : plan::kMaxRows) ||
+      mask_words < 0 || mask_words > plan::kMaxWords ||
+      (mask_words > 0 ? !dev_masks && n_rows > 0 : dev_masks != nullptr))
     return TL_EINVAL;
   const void* need[] = {dev_cached, dev_fresh, dev_block_table, dev_free_head, dev_cu, dev_lens, dev_granted,
                         dev_free_head_out};

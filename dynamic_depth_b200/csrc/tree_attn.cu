@@ -899,7 +899,7 @@ extern "C" int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_k
   if (n_heads < 1 || n_heads % pool->n_kv_heads || R < 0 || R > tree::kMaxR || n_rows < 0 || max_pages < 1 ||
       max_nodes < 1 ||
       (out_dtype != TL_F32 && out_dtype != pool->dtype) || (n_rows > 1 && (q_stride < width || out_stride < width)) ||
-      (q_stride * 2) % 16 || (out_stride * os) % 16 || (dev_masks != nullptr) != (mask_words > 0) || mask_words < 0 ||
+      (q_stride * 2) % 16 || (out_stride * os) % 16 || (mask_words > 0 ? !dev_masks && n_rows > 0 : dev_masks != nullptr) || mask_words < 0 ||
       mask_words > tree::kMaxWords ||
       (dev_masks && max_nodes > 32 * (int64_t)mask_words) || !(scale >= 0.f) || scale > 1e38f ||
       (int64_t)max_nodes * (n_heads / pool->n_kv_heads) > tree::kMaxRows)

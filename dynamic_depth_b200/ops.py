@@ -137,10 +137,8 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
     head = _alloc((1,), (1,), i32)
     slots, pos = _alloc((n_rows,), (1,), torch.int64), _alloc((n_rows,), (1,), i32)
     masks = _alloc((n_rows, mask_words), (mask_words, 1), i32) if mask_words else None
-    # an empty tensor has no address; the library wants one where a mask is asked for
-    mp = None if masks is None else (masks.data_ptr() or cu.data_ptr())
     check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
-                              slots.data_ptr(), pos.data_ptr(), mp, st, _raw_stream(dev)), "tl_plan_batch")
+                              slots.data_ptr(), pos.data_ptr(), _at(masks), st, _raw_stream(dev)), "tl_plan_batch")
     return BatchPlan(cu, lens, granted, head, slots, pos, masks)
 
 

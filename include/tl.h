@@ -590,7 +590,7 @@ int tl_token_logprobs(const void* dev_logits, int32_t dtype, int64_t rows, int32
  * 1 <= R <= 8192; page_tokens a power of two, 1 .. 4096; mask_words 0 .. 8;
  * n_rows <= 2^30, and <= 2^20 with dev_parents;
  * dev_free_head_out must not be dev_free_head, nor dev_lens dev_cached.
- * NULL allowed: dev_parents, dev_masks (mask_words 0), dev_status. */
+ * NULL allowed: dev_parents, dev_masks (mask_words 0, or n_rows 0), dev_status. */
 int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
                   int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages, int32_t n_free,
                   const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows, int32_t mask_words,
@@ -644,7 +644,7 @@ int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t rows, int64_
  *     apart; dev_out: out_dtype TL_F32 or the pool's, the same shape, out_stride
  *     apart (both strides and addresses multiples of 16 bytes);
  *   dev_lse: fp32 [rows][n_heads] natural-log sum of exponentials, or NULL;
- *   n_rows: rows dev_q and dev_out hold;
+ *   n_rows: rows dev_q and dev_out hold; with 0 the pointers may be NULL;
  *   max_nodes: the most nodes a request has; with masks <= 32 * mask_words.
  *     A request with more nodes, with a negative length, with rows past n_rows
  *     or with positions past max_pages or 2^31 - 4096 is left out
