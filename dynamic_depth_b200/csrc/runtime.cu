@@ -208,6 +208,9 @@ static GsChoice gs_plan(int fmt, int N, int K, int group, int nmat, int n_sms, i
 static constexpr int kMaxTreeNodes = 256, kTreeMaskWords = kMaxTreeNodes / 32;
 static constexpr int kTreeInts = 32 + kMaxTreeNodes * (2 + 1 + 1 + 1 + 1 + kTreeMaskWords);
 static constexpr int kTreeSms = 148;  // SMs that the tree attention of a context uses, at most
+// Page length of the identity table on which a tree's positions are planned: the longest that tl_plan_batch takes.
+// Its slots are positions whatever the page length, so it need not be the cache's, which may be longer.
+static constexpr int kTreePlanPage = 4096;
 
 // Offsets of every workspace region (computed identically by tl_workspace_bytes and tl_create).
 struct Layout {
@@ -215,6 +218,7 @@ struct Layout {
   size_t page_elems;
   std::vector<size_t> mat_off;  // per matrix
   int max_nodes;                // of a tl_speculate_tree call
+  int tree_pages;               // of kTreePlanPage positions, for max_seq
   size_t tree_tab, tree_ws;     // its tables, and the attention's workspace
   size_t gains, rope, page_table, kv, lanes, h, h_in, hrows, rows[6], act_a, act_qkv, act_q, act_o, act_u,
       act_a16, act_o16, act_u16, attn_part, attn_counters, part_val, part_idx, tok_stage, L_stage,
@@ -303,7 +307,8 @@ static Layout make_layout(const tl_config* c) {
   L.b_casc = take(lanes * c->n_heads * (hd + 2) * 4);
   // tree speculation: node tables (kTreeInts words), an identity page table, and the attention's pieces
   L.max_nodes = (int)std::min<size_t>(kMaxTreeNodes, std::min<size_t>(lanes, L.max_prefill));
-  L.tree_tab = take((size_t)(kTreeInts + 2 * L.pages_per_seq) * 4);
+  L.tree_pages = (c->max_seq + kTreePlanPage - 1) / kTreePlanPage;
+  L.tree_tab = take((size_t)(kTreeInts + 2 * L.tree_pages) * 4);
   L.tree_ws = take(tree_attn_workspace(hd, L.max_nodes, kTreeSms));
   L.total = o;
   return L;
@@ -898,7 +903,7 @@ TreeTab tree_tab(tl_ctx* c) {
   t.path = t.positions + kMaxTreeNodes;
   t.masks = reinterpret_cast<uint32_t*>(t.path + kMaxTreeNodes);
   t.ident = t.path + kMaxTreeNodes * (1 + kTreeMaskWords);
-  t.table = t.ident + c->lay.pages_per_seq;
+  t.table = t.ident + c->lay.tree_pages;
   return t;
 }
 
@@ -2041,10 +2046,10 @@ static int speculate_tree_impl(tl_ctx* c, int lane, int n_new, int Ld, int Lv, c
   for (int i = 0; i < n_levels; ++i) first.push_back(first[i + 1] + (first[i + 1] - first[i]) * widths[i]);
   const int nodes = first[n_levels + 1], T = st.pos + 1;
   if ((int64_t)T + n_new + nodes - 2 > cfg.max_seq) return TL_EINVAL;
-  std::vector<int32_t> parents(nodes, -1), ident(c->lay.pages_per_seq);
+  std::vector<int32_t> parents(nodes, -1), ident(c->lay.tree_pages);
   for (int i = 0; i < n_levels; ++i)
     for (int j = first[i + 1]; j < first[i + 2]; ++j) parents[j] = first[i] + (j - first[i + 1]) / widths[i];
-  for (int i = 0; i < c->lay.pages_per_seq; ++i) ident[i] = i;
+  for (int i = 0; i < c->lay.tree_pages; ++i) ident[i] = i;
   const TreeTab tab = tree_tab(c);
   TL_CUDA(cudaMemcpyAsync(tab.parents, parents.data(), (size_t)nodes * 4, cudaMemcpyHostToDevice, c->stream));
   TL_CUDA(cudaMemcpyAsync(tab.ident, ident.data(), ident.size() * 4, cudaMemcpyHostToDevice, c->stream));
@@ -2068,11 +2073,11 @@ static int speculate_tree_impl(tl_ctx* c, int lane, int n_new, int Ld, int Lv, c
     const int levels = std::min(n_levels, n_new - (int)tokens.size() - 1);
     const int n = first[levels + 1];
     // positions, masks and key slots of the nodes: the plan of one request on an identity page table
-    const int32_t in[4] = {p0, n, (p0 + cfg.kv_page_tokens - 1) / cfg.kv_page_tokens, p0};
+    const int32_t in[4] = {p0, n, (p0 + kTreePlanPage - 1) / kTreePlanPage, p0};
     TL_CUDA(cudaMemcpyAsync(tab.cached, in, sizeof(in), cudaMemcpyHostToDevice, c->stream));
     TL_CUDA(cudaMemcpyAsync(tab.tokens, &tokens.back(), 4, cudaMemcpyHostToDevice, c->stream));
-    TL_TRY(tl_plan_batch(tab.cached, tab.fresh, 1, cfg.kv_page_tokens, tab.table, c->lay.pages_per_seq, tab.ident,
-                         c->lay.pages_per_seq, tab.free_head, tab.parents, n, kTreeMaskWords, tab.cu, tab.lens,
+    TL_TRY(tl_plan_batch(tab.cached, tab.fresh, 1, kTreePlanPage, tab.table, c->lay.tree_pages, tab.ident,
+                         c->lay.tree_pages, tab.free_head, tab.parents, n, kTreeMaskWords, tab.cu, tab.lens,
                          tab.granted, tab.head_out, tab.slots, tab.positions, tab.masks, c->status, c->stream));
     c->launches++;
     // draft: a level at a time at L_draft, the best tokens of each node become its children

@@ -4,7 +4,11 @@ import pytest
 import torch
 
 import dynamic_depth_b200 as T
+import synthetic as S
+from gpu_helpers import gpu_model, oracle_weights, status_clean
+from oracle import decode as D
 from test_gpu_operators import F16
+from test_gpu_speculate_tree import nodes_of, stop_at
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +30,36 @@ def test_an_empty_batch_goes_through_every_operator():
         lp = T.token_logprobs(out.reshape(0, 256), torch.zeros(0, **i32), n_top=3)
         assert lp.top_ids.shape == (0, 3) and lp.logprob.shape == (0,)
     assert bool((pool == 1).all())
+
+
+@pytest.mark.parametrize("page", [4096, 8192, 1 << 15])
+def test_tree_speculation_on_a_context_with_long_pages(page):
+    W, widths, n_new = oracle_weights("tiny"), [2, 2], 7
+    P = S.prompts(1, 11, 512, seed=141)[0]
+    m = gpu_model("tiny", None, max_lanes=nodes_of(widths), max_seq=32, L_max=3, max_prefill_tokens=16,
+                  kv_page_tokens=page)
+    plain = D.generate_lane(W, P, 3, n_new)
+    stop = stop_at(plain)
+    assert stop > 1
+    m.prefill(0, P, 3)
+    chain, _ = m.speculate(0, n_new, 1, 3, 2)
+    assert chain[:stop].tolist() == plain.tokens[:stop].tolist()
+    m.prefill(0, P, 3)
+    tok, _ = m.speculate_tree(0, n_new, 1, 3, widths)
+    status_clean(m)
+    assert tok[:stop].tolist() == plain.tokens[:stop].tolist()
+
+
+def test_tree_speculation_across_position_4096():
+    """Prompts that end before and behind the end of a planning page, nodes on both sides of it; the tokens are those of
+    a chain of drafts."""
+    n_new, widths = 10, [2, 2]
+    m = gpu_model("tiny", None, max_lanes=nodes_of(widths), max_seq=4096 + 64, L_max=2, max_prefill_tokens=4200)
+    for T_ in (4089, 4096, 4099):
+        P = S.prompts(1, T_, 512, seed=143)[0]
+        m.prefill(0, P, 2)
+        chain, _ = m.speculate(0, n_new, 1, 2, 2)
+        m.prefill(0, P, 2)
+        tok, _ = m.speculate_tree(0, n_new, 1, 2, widths)
+        status_clean(m)
+        assert tok.tolist() == chain.tolist()
