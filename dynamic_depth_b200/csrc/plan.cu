@@ -210,7 +210,19 @@ extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh
   if (((uintptr_t)dev_free_pages & 3) || ((uintptr_t)dev_slots & 7) || ((uintptr_t)dev_positions & 3) ||
       ((uintptr_t)dev_masks & 3) || ((uintptr_t)dev_parents & 3) || ((uintptr_t)dev_status & 3))
     return TL_EINVAL;
-  if (dev_free_head_out == dev_free_head || dev_lens == dev_cached) return TL_EINVAL;
+  // the CTAs read the inputs while others write: an output shares no byte with an input or another output
+  const size_t nr = (size_t)n_rows, nR = (size_t)R;
+  const Buf ins[] = {{dev_cached, 4 * nR}, {dev_fresh, 4 * nR}, {dev_free_pages, 4 * (size_t)n_free},
+                     {dev_free_head, 4}, {dev_parents, 4 * nr}};
+  const Buf outs[] = {{dev_block_table, 4 * nR * max_pages}, {dev_cu, 4 * nR + 4}, {dev_lens, 4 * nR},
+                      {dev_granted, 4 * nR}, {dev_free_head_out, 4}, {dev_slots, 8 * nr}, {dev_positions, 4 * nr},
+                      {dev_masks, 4 * nr * mask_words}, {dev_status, 4}};
+  for (const Buf& o : outs) {
+    for (const Buf& i : ins)
+      if (share_bytes(o, i)) return TL_EINVAL;
+    for (const Buf* q = &o + 1; q < outs + sizeof(outs) / sizeof(outs[0]); ++q)
+      if (share_bytes(o, *q)) return TL_EINVAL;
+  }
   plan::Args a{dev_cached, dev_fresh, R, 0, max_pages, dev_block_table, dev_free_pages, n_free, dev_free_head,
                dev_parents, n_rows, mask_words, dev_cu, dev_lens, dev_granted, dev_free_head_out, dev_slots,
                dev_positions, dev_masks, dev_status};

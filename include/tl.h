@@ -589,7 +589,8 @@ int tl_token_logprobs(const void* dev_logits, int32_t dtype, int64_t rows, int32
  * dev_fresh above 2^24, counts as 0 and is refused (TL_BAD_LENGTH).
  * 1 <= R <= 8192; page_tokens a power of two, 1 .. 4096; mask_words 0 .. 8;
  * n_rows <= 2^30, and <= 2^20 with dev_parents;
- * dev_free_head_out must not be dev_free_head, nor dev_lens dev_cached.
+ * No output (the block table and dev_status among them) shares a byte with an
+ * input or another output.
  * NULL allowed: dev_parents, dev_masks (mask_words 0, or n_rows 0), dev_status. */
 int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
                   int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages, int32_t n_free,

@@ -25,3 +25,25 @@ def test_tree_attention_of_no_rows_needs_no_masks(R, rows):
 def test_masks_are_still_wanted_where_there_are_rows():
     assert _lib.lib().tl_tree_attention(A, 128, pool(), A, 4, A, A, 2, 3, 2, 8, None, 1, 0.0, A, _lib.TL_F16, 128, None,
                                         A, 1 << 30, None, None) == _lib.TL_EINVAL
+
+
+# buffers of a plan of 5 requests and 7 rows, each at an address of its own, and their sizes in bytes
+PLAN = dict(cached=20, fresh=20, table=80, free=12, free_head=4, parents=28, cu=24, lens=20, granted=20, head_out=4,
+            slots=56, positions=28, masks=56, status=4)
+OUTPUTS = ("table", "cu", "lens", "granted", "head_out", "slots", "positions", "masks", "status")
+
+
+@pytest.mark.parametrize("out", OUTPUTS)
+def test_plan_outputs_share_no_byte_with_another_buffer(out):
+    def plan(at):
+        return _lib.lib().tl_plan_batch(at["cached"], at["fresh"], 5, 16, at["table"], 4, at["free"], 3,
+                                        at["free_head"], at["parents"], 7, 2, at["cu"], at["lens"], at["granted"],
+                                        at["head_out"], at["slots"], at["positions"], at["masks"], at["status"], None)
+    apart = {k: A + 4096 * i for i, k in enumerate(PLAN)}
+    for other, size in PLAN.items():
+        if other == out:
+            continue
+        first = apart[other]
+        last = first + size - (8 if out == "slots" else 4)  # the last place of the other's that this one's can start in
+        for at in {first, max(first, last // 8 * 8 if out == "slots" else last)}:
+            assert plan(dict(apart, **{out: at})) == _lib.TL_EINVAL, (other, at - first)
