@@ -2,7 +2,9 @@
 import ctypes as C
 
 import pytest
+import torch
 
+import dynamic_depth_b200 as T
 from dynamic_depth_b200 import _lib
 
 A = 0x100000  # an aligned address that nothing reads
@@ -47,3 +49,33 @@ def test_plan_outputs_share_no_byte_with_another_buffer(out):
         last = first + size - (8 if out == "slots" else 4)  # the last place of the other's that this one's can start in
         for at in {first, max(first, last // 8 * 8 if out == "slots" else last)}:
             assert plan(dict(apart, **{out: at})) == _lib.TL_EINVAL, (other, at - first)
+
+
+def _calls():
+    """One call of each operator with floating inputs: the call and the names of those inputs."""
+    z = torch.zeros(2, dtype=torch.int32)
+    h = dict(dtype=torch.float16)
+
+    def make():
+        return dict(logits=torch.zeros(2, 5), qkv=torch.zeros(2, 192, **h), pool=torch.zeros(2, 2, 1, 16, 64, **h),
+                    rope=torch.zeros(4, 32, 2), q_gain=torch.ones(64), k_gain=torch.ones(64),
+                    q=torch.zeros(2, 1, 64, **h), out=torch.zeros(2, 1, 64, **h))
+    return make, [
+        (lambda d: T.token_logprobs(d["logits"], n_top=1), ("logits",)),
+        (lambda d: T.norm_rope_append(d["qkv"], 1, d["pool"], z.long(), z, d["rope"], q_gain=d["q_gain"],
+                                      k_gain=d["k_gain"], q_out=d["out"]),
+         ("qkv", "pool", "rope", "q_gain", "k_gain", "out")),
+        (lambda d: T.tree_attention(d["q"], d["pool"], torch.zeros(1, 4, dtype=torch.int32), z[:1], z, 1, out=d["out"]),
+         ("q", "pool", "out"))]
+
+
+def test_tensors_that_want_a_gradient_are_refused():
+    make, calls = _calls()
+    for call, names in calls:
+        for name in names:
+            d = make()
+            d[name].requires_grad_(True)
+            with pytest.raises(ValueError, match="backward"):
+                call(d)
+            with torch.no_grad(), pytest.raises(ValueError, match="cuda|CUDA|device"):  # host tensors: refused as such
+                call(d)
