@@ -440,7 +440,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const TreeAttnArgs a
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = e & 1, col = kk * 16 + c0 + (e >> 1) * 8;
-            qf[kk][e] = node[i] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(qp[i] + col * 2)) : 0u;
+            // (no read-only load: the output may take the queries' place, row block by row block)
+            qf[kk][e] = node[i] >= 0 ? *reinterpret_cast<const uint32_t*>(qp[i] + col * 2) : 0u;
           }
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float O[HD / 8][4];
@@ -910,6 +911,16 @@ extern "C" int tl_tree_attention(const void* dev_q, int64_t q_stride, const tl_k
       ((uintptr_t)dev_ctx & 3) || ((uintptr_t)dev_cu & 3) || ((uintptr_t)dev_masks & 3) || ((uintptr_t)dev_lse & 3) ||
       ((uintptr_t)dev_workspace & 255) || ((uintptr_t)dev_status & 3))
     return TL_EINVAL;
+  // The output may be the queries' own place: a row block is written by the one CTA that read its queries, or by the
+  // joining kernel.  Any other overlap lets one block's output overwrite another's queries; rows that only interleave
+  // share nothing.
+  const int64_t rows1 = n_rows - 1, qb = q_stride * 2, ob = out_stride * os, qw = width * 2, ow = width * os;
+  const bool same = dev_q == dev_out && os == 2 && (rows1 == 0 || qb == ob);
+  if (!same && share_bytes({dev_q, (size_t)(rows1 * qb + qw)}, {dev_out, (size_t)(rows1 * ob + ow)})) {
+    if (rows1 == 0 || qb != ob) return TL_EINVAL;
+    const int64_t d = (int64_t)((intptr_t)dev_out - (intptr_t)dev_q) % qb, at = d < 0 ? d + qb : d;
+    if (at < qw || at + ow > qb) return TL_EINVAL;
+  }
   size_t need = 0;
   TL_TRY(tl_tree_attention_workspace(pool->head_dim, n_heads, pool->n_kv_heads, max_nodes, &need));
   if (workspace_bytes < need) return TL_ENOMEM;

@@ -215,7 +215,8 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
                    return_lse: bool = False, workspace=None, status=None):
     """Attention of draft trees over the pool's pages: rows cu[r] .. cu[r+1] of q [rows, heads, width] see request r's
     first ctx_lens[r] positions and the nodes behind them that their mask words name (None: the earlier nodes and
-    themselves).  out: a given tensor's type (the pool's or fp32), else the pool's.  Returns out, or (out, lse)."""
+    themselves).  out: a given tensor's type (the pool's or fp32), else the pool's; it may be q.  Returns out, or
+    (out, lse)."""
     _forward_only(q, pool, out)
     p = _pool(pool)
     dev, hd = pool.get_device(), p.head_dim

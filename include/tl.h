@@ -643,7 +643,9 @@ int tl_norm_rope_append(const void* dev_qkv, int32_t dtype, int64_t rows, int64_
  * they are.
  *   dev_q: the pool's dtype, rows of [n_heads][head_dim], q_stride elements
  *     apart; dev_out: out_dtype TL_F32 or the pool's, the same shape, out_stride
- *     apart (both strides and addresses multiples of 16 bytes);
+ *     apart (both strides and addresses multiples of 16 bytes).  dev_out may be
+ *     dev_q, in its type and with its stride; otherwise their rows share no byte
+ *     (TL_EINVAL);
  *   dev_lse: fp32 [rows][n_heads] natural-log sum of exponentials, or NULL;
  *   n_rows: rows dev_q and dev_out hold; with 0 the pointers may be NULL;
  *   max_nodes: the most nodes a request has; with masks <= 32 * mask_words.

@@ -7,7 +7,7 @@ import dynamic_depth_b200 as T
 import synthetic as S
 from gpu_helpers import gpu_model, oracle_weights, status_clean
 from oracle import decode as D
-from test_gpu_operators import F16
+from test_gpu_operators import BF16, F16, run_tree, tree_case
 from test_gpu_speculate_tree import nodes_of, stop_at
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,23 @@ def test_tree_speculation_across_position_4096():
         tok, _ = m.speculate_tree(0, n_new, 1, 2, widths)
         status_clean(m)
         assert tok.tolist() == chain.tolist()
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("nodes", [3, 12, 70])
+def test_outputs_in_the_queries_own_place(hd, nodes):
+    """dev_out may be dev_q: whole row blocks, and blocks cut over several CTAs."""
+    c = tree_case([2500, 40, 0, 700], [nodes, 2, nodes, 1], 8, 2, hd, BF16, 32, seed=hd + nodes)
+    want, wl, _ = run_tree(c)
+    o, lse, st = run_tree(c, out=c["q"])
+    assert st == 0 and o.data_ptr() == c["q"].data_ptr()
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+def test_queries_and_outputs_side_by_side_in_one_buffer():
+    c = tree_case([300, 9], [5, 8], 4, 2, 64, F16, 16, seed=20)
+    want, _, _ = run_tree(c)
+    wide = torch.zeros(13, 2, 4, 64, dtype=F16, device="cuda")
+    wide[:, 0] = c["q"]
+    c["q"] = wide[:, 0]
+    assert torch.equal(run_tree(c, out=wide[:, 1])[0], want)

@@ -79,3 +79,26 @@ def test_tensors_that_want_a_gradient_are_refused():
                 call(d)
             with torch.no_grad(), pytest.raises(ValueError, match="cuda|CUDA|device"):  # host tensors: refused as such
                 call(d)
+
+
+@pytest.mark.parametrize("out,stride,dtype,rows", [
+    (A + 16, 128, _lib.TL_F16, 3),           # inside the first row
+    (A + 256, 128, _lib.TL_F16, 3),          # the next row
+    (A - 256, 128, _lib.TL_F16, 3),
+    (A, 256, _lib.TL_F16, 3),                # the same place with another stride
+    (A, 128, _lib.TL_F32, 3),                # and with another type
+    (A + 256, 256, _lib.TL_F16, 2),
+    (A, 128, _lib.TL_F32, 1),
+    (A + 16, 128, _lib.TL_F16, 1)])
+def test_attention_outputs_beside_the_queries_or_in_their_place(out, stride, dtype, rows):
+    st = _lib.lib().tl_tree_attention(A, 128, pool(dev_pool=2 * A), 3 * A, 4, 3 * A, 3 * A, 2, rows, 2, 8, None, 0, 0.0, out,
+                                      dtype, stride, None, 4 * A, 1 << 30, None, None)
+    assert st == _lib.TL_EINVAL
+
+
+@pytest.mark.parametrize("shift", [16, 240, 272, 512 - 16, -16, -240, 512 + 128])
+def test_attention_outputs_between_the_queries_rows(shift):
+    """Rows of 256 bytes every 512: an output shifted by 256 fits between them, one shifted by less or more does not."""
+    st = _lib.lib().tl_tree_attention(A, 256, pool(dev_pool=2 * A), 3 * A, 4, 3 * A, 3 * A, 2, 5, 2, 8, None, 0, 0.0,
+                                      A + shift, _lib.TL_F16, 256, None, 4 * A, 1 << 30, None, None)
+    assert st == _lib.TL_EINVAL
