@@ -47,11 +47,14 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _forward_only(*tensors):
+def _forward_only():
+    """A call was given a tensor that requires a gradient."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("no backward form: detach the tensors or call under torch.no_grad()")
+        raise ValueError("no backward form: detach the tensors or call under torch.no_grad()")
+
+
+def _wants(t):
+    return t is not None and t.requires_grad
 
 
 def _flat(t, dtype, n, name, dev):
@@ -96,7 +99,8 @@ def _pool(pool) -> TlKvPool:
 def token_logprobs(logits, targets=None, n_top: int = 0) -> TokenLogprobs:
     """Log probability and rank of each row's target, entropy, log-sum-exp and the n_top best tokens of logits
     [rows, vocab] (fp32, fp16 or bf16; rows may be strided).  targets int32 [rows], -1 for none."""
-    _forward_only(logits)
+    if logits.requires_grad:
+        _forward_only()
     _need(logits.dim() == 2 and logits.dtype in _DT and (logits.shape[1] <= 1 or logits.stride(1) == 1),
           "logits: [rows, vocab] of fp32, fp16 or bf16 with adjacent columns is wanted")
     rows, vocab = logits.shape
@@ -167,7 +171,8 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
                      q_out=None, status=None) -> torch.Tensor:
     """Per-head RMSNorm (with gains) and rotation of the queries and keys of qkv [rows, (q | k | v) heads * width],
     keys and values stored at `slots` of the pool; returns the queries [rows, n_heads, width] in the pool's type."""
-    _forward_only(qkv, pool, rope, q_gain, k_gain, q_out)
+    if qkv.requires_grad or pool.requires_grad or rope.requires_grad or _wants(q_gain) or _wants(k_gain) or _wants(q_out):
+        _forward_only()
     p = _pool(pool)
     dev, rows, hd = pool.get_device(), qkv.shape[0], p.head_dim
     _need(qkv.dim() == 2 and qkv.dtype in _DT and qkv.shape[1] == (n_heads + 2 * p.n_kv_heads) * hd
@@ -217,7 +222,8 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
     first ctx_lens[r] positions and the nodes behind them that their mask words name (None: the earlier nodes and
     themselves).  out: a given tensor's type (the pool's or fp32), else the pool's; it may be q.  Returns out, or
     (out, lse)."""
-    _forward_only(q, pool, out)
+    if q.requires_grad or pool.requires_grad or _wants(out):
+        _forward_only()
     p = _pool(pool)
     dev, hd = pool.get_device(), p.head_dim
     _need(q.dim() == 3 and q.dtype == pool.dtype and q.shape[2] == hd and q.stride(2) == 1
