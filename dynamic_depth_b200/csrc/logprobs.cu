@@ -40,6 +40,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kCand = 2048;      // candidates ordered in shared memory; more take the extraction loop
 constexpr int kList = 256;       // chunks that reach the bound; more take the exact search
 constexpr int kWarpCand = 256;   // candidates of a row that one warp handles
+constexpr int kWarpTop = 56;     // most best tokens of such a row (see launch)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -846,8 +847,11 @@ static int launch(Args a, cudaStream_t s) {
   int dev = 0, sms = 0;
   TL_CUDA(cudaGetDevice(&dev));
   TL_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  // many short rows: a warp a row
-  const bool by_warp = a.V + 8 <= 64 * kChunk && a.rows >= 8 * sms;
+  // Many short rows: a warp a row, unless so many of the best are wanted that ordinary rows hold more than kWarpCand
+  // candidates (the bound is the n-th of 64 maxima: at n = 64 some 300 elements reach the lowest of them) and would be
+  // read once per token wanted.  4000 x 8000 bf16, a warp against a CTA a row: n 20 38 / 65 us, n 56 70 / 96, n 60
+  // 605 / 110, n 64 2,991 / 186; 4000 x 16000: n 56 97 / 120, n 58 589 / 124; 1300 x 3001 fp32: n 56 31 / 30.
+  const bool by_warp = a.V + 8 <= 64 * kChunk && a.rows >= 8 * sms && a.n_top <= kWarpTop;
   // CTAs of a row: as many as fill the SMs at most once (a second wave of them costs more than the first saves:
   // 128 x 131072 bf16 took 16 us with 2 CTAs a row and 31 us with 8), each with 2 groups of chunks a warp or more
   int cs = 1;

@@ -1,5 +1,7 @@
 """What the serving operators promise beyond their sums: empty batches, buffers that overlap, capture into graphs,
 contexts with long pages, and a serving step checked stage by stage."""
+import math
+
 import pytest
 import torch
 
@@ -7,7 +9,7 @@ import dynamic_depth_b200 as T
 import synthetic as S
 from gpu_helpers import gpu_model, oracle_weights, status_clean
 from oracle import decode as D
-from test_gpu_operators import BF16, F16, run_tree, tree_case
+from test_gpu_operators import BF16, F16, gen, run_tree, tree_case
 from test_gpu_speculate_tree import nodes_of, stop_at
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +85,23 @@ def test_queries_and_outputs_side_by_side_in_one_buffer():
     wide[:, 0] = c["q"]
     c["q"] = wide[:, 0]
     assert torch.equal(run_tree(c, out=wide[:, 1])[0], want)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1300, 9000), (4000, 16000)])
+def test_the_cost_of_many_best_tokens_has_no_step(rows, vocab):
+    """Ordinary (normal) rows: 64 best tokens cost a few times what 40 do, not a pass over the row for each of them."""
+    x = (torch.randn(rows, vocab, generator=gen(vocab), device="cuda") * 3).bfloat16()
+    cost = {}
+    for n in (40, 57, 60, 64):
+        T.token_logprobs(x, n_top=n)
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            o = T.token_logprobs(x, n_top=n)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        cost[n] = best
+        assert torch.equal(o.top_logprobs, o.top_logprobs.sort(1, descending=True).values)
+    assert max(cost.values()) < 8 * cost[40], cost
