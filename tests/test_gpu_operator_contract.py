@@ -2,14 +2,16 @@
 contexts with long pages, and a serving step checked stage by stage."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import dynamic_depth_b200 as T
+import operator_refs as R
 import synthetic as S
 from gpu_helpers import gpu_model, oracle_weights, status_clean
 from oracle import decode as D
-from test_gpu_operators import BF16, F16, gen, run_tree, tree_case
+from test_gpu_operators import BF16, F16, gen, random_tree, run_tree, tree_case
 from test_gpu_speculate_tree import nodes_of, stop_at
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +107,90 @@ def test_the_cost_of_many_best_tokens_has_no_step(rows, vocab):
         cost[n] = best
         assert torch.equal(o.top_logprobs, o.top_logprobs.sort(1, descending=True).values)
     assert max(cost.values()) < 8 * cost[40], cost
+
+
+def test_a_serving_step_checked_stage_by_stage():
+    """Plan, append, attention and log probabilities of a prompt, a tree of drafts and a block of single tokens, captured
+    in one graph a step; each stage is checked on what the one before it left, so its bound is its own rounding alone."""
+    g, rng = gen(30), np.random.default_rng(30)
+    H, Hk, hd, page, n_pages, base, V = 8, 2, 64, 16, 64, 1e4, 999
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    pool = torch.zeros(n_pages, 2, Hk, page, hd, dtype=BF16, device="cuda")
+    table = torch.full((3, 12), -1, **i32)
+    free = torch.from_numpy(rng.permutation(n_pages).astype(np.int32)).cuda()
+    head, lens = torch.zeros(1, **i32), torch.zeros(3, **i32)
+    rope = T.rope_table(256, hd, base)
+    gq, gk = (1 + 0.1 * torch.randn(hd, generator=g, device="cuda") for _ in range(2))
+    w = torch.randn(H * hd, V, generator=g, device="cuda") / 20
+    half, fp = R.HALF_STEP[BF16], (hd / 16 + 12) * 2.0 ** -24
+    for fresh, tree in (([40, 7, 90], False), ([9, 1, 14], True), ([1, 1, 1], False)):
+        total = sum(fresh)
+        parents = sum((random_tree(rng, f) for f in fresh), []) if tree else None
+        x = torch.randn(total, (H + 2 * Hk) * hd, generator=g, device="cuda").to(BF16)
+        ins = (lens.clone(), torch.tensor(fresh, **i32), head.clone(), torch.tensor(parents, **i32) if tree else None,
+               torch.zeros(total, **i32))
+        np_table, ctx, old_head = table.cpu().numpy(), lens.tolist(), int(head)
+        before = pool.clone()
+
+        def step():
+            plan = T.plan_batch(ins[0], ins[1], table, free, ins[2], page, total, parents=ins[3],
+                                mask_words=1 if tree else 0)
+            q = T.norm_rope_append(x, H, pool, plan.slots, plan.positions, rope, q_gain=gq, k_gain=gk)
+            out, lse = T.tree_attention(q, pool, table, ins[0], plan.cu, max(fresh), masks=plan.masks, return_lse=True)
+            logits = (out.reshape(total, -1).float() @ w).contiguous()
+            return plan, q, out, lse, logits, T.token_logprobs(logits, ins[4], n_top=3)
+        torch.mm(torch.zeros(2, 2, device="cuda"), torch.zeros(2, 2, device="cuda"))  # the library's handle, before capture
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan, q, out, lse, logits, lp = step()
+        assert torch.equal(pool, before)  # captured, not run
+        graph.replay()
+        torch.cuda.synchronize()
+        # the plan, exactly
+        want = R.plan(ctx, fresh, np_table, free.cpu().numpy(), old_head, page, parents, 1 if tree else 0)
+        assert np.array_equal(table.cpu().numpy(), np_table) and plan.slots.tolist() == want["slots"]
+        assert plan.positions.tolist() == want["positions"] and plan.lens.tolist() == want["lens"]
+        # norm, rotation and append
+        wq, wk, wv, sq, sk = R.norm_rope(n64(x), H, Hk, hd, np.array(want["positions"]), base, n64(gq), n64(gk))
+        flat = n64(pool.permute(0, 3, 1, 2, 4).reshape(-1, 2, Hk, hd)[plan.slots])
+        assert (np.abs(n64(q) - wq) <= half * np.abs(wq) + fp * sq).all()
+        assert (np.abs(flat[:, 0] - wk) <= half * np.abs(wk) + fp * sk).all() and np.array_equal(flat[:, 1], wv)
+        # attention, on the queries and the cache as they are, masks from the parents by hand
+        see = None
+        if tree:
+            see = np.zeros((total, 32), bool)
+            for r in range(3):
+                for j in range(fresh[r]):
+                    row = want["cu"][r] + j
+                    if parents[row] >= 0:
+                        see[row] = see[want["cu"][r] + parents[row]]
+                    see[row, j] = True
+        wo, wl, tol, ltol = R.tree_attention(n64(q), n64(pool), np_table, ctx, want["cu"], see, hd ** -0.5, BF16)
+        assert (np.abs(n64(out) - wo) <= tol).all() and (np.abs(n64(lse) - wl) <= ltol).all()
+        # log probabilities of the logits as they are
+        for r in range(total):
+            p, rank, ent, ls, ids, top = R.logprobs_row(n64(logits[r]), 0, 3)
+            e = 2 * R.sum_bound(V / 256 + 8)
+            assert int(lp.rank[r]) == rank and lp.top_ids[r].tolist() == ids.tolist()
+            assert abs(float(lp.logprob[r]) - p) <= e + 2.0 ** -23 * abs(p)
+            assert abs(float(lp.lse[r]) - ls) <= e + 2.0 ** -23 * abs(ls)
+            assert abs(float(lp.entropy[r]) - ent) <= e * (1 + ent) + 2.0 ** -23 * ent
+        lens, head = plan.lens.clone(), plan.free_head.clone()
+    assert lens.tolist() == [50, 9, 105]
+
+
+@pytest.mark.parametrize("name,widths", [("tiny", [3, 3]), ("m407", [4, 2, 2])])
+def test_tree_speculation_with_split_activations(name, widths):
+    """More than 8 nodes a pass, so the projections run on the tensor cores and read the attention's output as high
+    and low fp16 halves."""
+    sh, W, n = S.SHAPES[name], oracle_weights(name), nodes_of(widths)
+    P, n_new = S.prompts(1, 17, sh.vocab, seed=142)[0], 7
+    m = gpu_model(name, None, max_lanes=n, max_seq=17 + n_new + n, L_max=4, max_prefill_tokens=32, act_split=1)
+    plain = D.generate_lane(W, P, 4, n_new)
+    stop = stop_at(plain)
+    assert stop > 1
+    m.prefill(0, P, 4)
+    tok, _ = m.speculate_tree(0, n_new, 2, 4, widths)
+    status_clean(m)
+    assert tok[:stop].tolist() == plain.tokens[:stop].tolist()
