@@ -105,6 +105,7 @@ SIGNATURES = {
     "tl_strerror": (C.c_char_p, [C.c_int]),
     "tl_last_cuda_error": (C.c_char_p, []),
 }
+SIGNATURES["tl_plan_batch_padded"] = SIGNATURES["tl_plan_batch"]
 
 _lib = None
 

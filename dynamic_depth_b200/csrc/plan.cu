@@ -38,6 +38,7 @@ struct Args {
   int32_t* positions;
   uint32_t* masks;
   int32_t* status;
+  int32_t pad;  // rows behind the batch: 1 written as rows of no token, 0 left as they are
 };
 
 struct Req {
@@ -133,8 +134,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
   }
   // the rows
   int bad = 0;
-  const int n = min(total, a.n_rows);
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
+  const int n = min(total, a.n_rows), upto = a.pad ? a.n_rows : n;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < upto; i += gridDim.x * kThreads) {
+    if (i >= n) {
+      a.slots[i] = -1;
+      a.positions[i] = 0;
+      for (int w = 0; a.masks && w < a.words; ++w) a.masks[(int64_t)i * a.words + w] = 0u;
+      continue;
+    }
     int lo = 0, hi = a.R;  // the last request with cu <= i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -186,17 +193,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(Args a) {
   if (a.status && bad) atomicOr(a.status, bad);
 }
 
-}  // namespace plan
-}  // namespace tl
-
-using namespace tl;
-
-extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
-                             int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages,
-                             int32_t n_free, const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows,
-                             int32_t mask_words, int32_t* dev_cu, int32_t* dev_lens, int32_t* dev_granted,
-                             int32_t* dev_free_head_out, int64_t* dev_slots, int32_t* dev_positions,
-                             uint32_t* dev_masks, int32_t* dev_status, void* cuda_stream) {
+static int plan_batch(bool pad, const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
+                      int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages, int32_t n_free,
+                      const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows, int32_t mask_words,
+                      int32_t* dev_cu, int32_t* dev_lens, int32_t* dev_granted, int32_t* dev_free_head_out,
+                      int64_t* dev_slots, int32_t* dev_positions, uint32_t* dev_masks, int32_t* dev_status,
+                      void* cuda_stream) {
   if (R < 1 || R > plan::kMaxR || page_tokens < 1 || page_tokens > 4096 || (page_tokens & (page_tokens - 1)) ||
       max_pages < 1 || n_free < 0 || n_rows < 0 || n_rows > (dev_parents ? plan::kMaxTreeRows : plan::kMaxRows) ||
       mask_words < 0 || mask_words > plan::kMaxWords ||
@@ -225,7 +227,7 @@ extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh
   }
   plan::Args a{dev_cached, dev_fresh, R, 0, max_pages, dev_block_table, dev_free_pages, n_free, dev_free_head,
                dev_parents, n_rows, mask_words, dev_cu, dev_lens, dev_granted, dev_free_head_out, dev_slots,
-               dev_positions, dev_masks, dev_status};
+               dev_positions, dev_masks, dev_status, pad};
   while ((1 << a.shift) < page_tokens) ++a.shift;
   const size_t smem = (size_t)(2 * R + 1) * 4;  // at most 64 KB
   if (smem > 46 * 1024)
@@ -235,4 +237,30 @@ extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh
   const int64_t grid = by_rows > by_req ? by_rows : by_req;
   plan::plan_kernel<<<(unsigned)(grid < 592 ? grid : 592), plan::kThreads, smem, (cudaStream_t)cuda_stream>>>(a);
   return check_cuda(cudaGetLastError());
+}
+
+}  // namespace plan
+}  // namespace tl
+
+extern "C" int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
+                             int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages,
+                             int32_t n_free, const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows,
+                             int32_t mask_words, int32_t* dev_cu, int32_t* dev_lens, int32_t* dev_granted,
+                             int32_t* dev_free_head_out, int64_t* dev_slots, int32_t* dev_positions,
+                             uint32_t* dev_masks, int32_t* dev_status, void* cuda_stream) {
+  return tl::plan::plan_batch(false, dev_cached, dev_fresh, R, page_tokens, dev_block_table, max_pages, dev_free_pages,
+                              n_free, dev_free_head, dev_parents, n_rows, mask_words, dev_cu, dev_lens, dev_granted,
+                              dev_free_head_out, dev_slots, dev_positions, dev_masks, dev_status, cuda_stream);
+}
+
+extern "C" int tl_plan_batch_padded(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R,
+                                    int32_t page_tokens, int32_t* dev_block_table, int32_t max_pages,
+                                    const int32_t* dev_free_pages, int32_t n_free, const int32_t* dev_free_head,
+                                    const int32_t* dev_parents, int32_t n_rows, int32_t mask_words, int32_t* dev_cu,
+                                    int32_t* dev_lens, int32_t* dev_granted, int32_t* dev_free_head_out,
+                                    int64_t* dev_slots, int32_t* dev_positions, uint32_t* dev_masks,
+                                    int32_t* dev_status, void* cuda_stream) {
+  return tl::plan::plan_batch(true, dev_cached, dev_fresh, R, page_tokens, dev_block_table, max_pages, dev_free_pages,
+                              n_free, dev_free_head, dev_parents, n_rows, mask_words, dev_cu, dev_lens, dev_granted,
+                              dev_free_head_out, dev_slots, dev_positions, dev_masks, dev_status, cuda_stream);
 }

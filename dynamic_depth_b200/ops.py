@@ -129,7 +129,7 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
                mask_words: int = 0, status=None) -> BatchPlan:
     """Row offsets, slots, positions and tree masks of a batch's new tokens from the request lengths; the block table
     [R, max_pages] (int32) gets the pages granted from free_pages[free_head[0]:].  n_rows: rows of the row outputs
-    (at least the sum of fresh; rows past that sum are not written)."""
+    (at least the sum of fresh; rows past that sum are rows of no token: slot -1, position 0, no mask bits)."""
     R = cached.numel()
     dev = cached.get_device()
     _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32
@@ -153,8 +153,9 @@ def plan_batch(cached, fresh, block_table, free_pages, free_head, page_tokens: i
     head = _alloc((1,), (1,), i32)
     slots, pos = _alloc((n_rows,), (1,), torch.int64), _alloc((n_rows,), (1,), i32)
     masks = _alloc((n_rows, mask_words), (mask_words, 1), i32) if mask_words else None
-    check(lib().tl_plan_batch(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
-                              slots.data_ptr(), pos.data_ptr(), _at(masks), st, _raw_stream(dev)), "tl_plan_batch")
+    check(lib().tl_plan_batch_padded(*args, cu.data_ptr(), lens.data_ptr(), granted.data_ptr(), head.data_ptr(),
+                                     slots.data_ptr(), pos.data_ptr(), _at(masks), st, _raw_stream(dev)),
+          "tl_plan_batch_padded")
     return BatchPlan(cu, lens, granted, head, slots, pos, masks)
 
 

@@ -599,6 +599,16 @@ int tl_plan_batch(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R
                   int64_t* dev_slots, int32_t* dev_positions, uint32_t* dev_masks, int32_t* dev_status,
                   void* cuda_stream);
 
+/* tl_plan_batch for a batch of a fixed number of rows: rows from cu[R] on are
+ * written as rows of no token (slot -1, position 0, no mask bits), so that
+ * tl_norm_rope_append may be given all n_rows and stores nothing for them. */
+int tl_plan_batch_padded(const int32_t* dev_cached, const int32_t* dev_fresh, int32_t R, int32_t page_tokens,
+                         int32_t* dev_block_table, int32_t max_pages, const int32_t* dev_free_pages, int32_t n_free,
+                         const int32_t* dev_free_head, const int32_t* dev_parents, int32_t n_rows, int32_t mask_words,
+                         int32_t* dev_cu, int32_t* dev_lens, int32_t* dev_granted, int32_t* dev_free_head_out,
+                         int64_t* dev_slots, int32_t* dev_positions, uint32_t* dev_masks, int32_t* dev_status,
+                         void* cuda_stream);
+
 /* Rotation table: dev_table fp32 [length][head_dim / 2][2] = (cos, sin) of
  * position * base^(-2i / head_dim), angles in fp64. */
 int tl_rope_table(float* dev_table, int32_t length, int32_t head_dim, double base, void* cuda_stream);

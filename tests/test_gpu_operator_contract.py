@@ -194,3 +194,29 @@ def test_tree_speculation_with_split_activations(name, widths):
     tok, _ = m.speculate_tree(0, n_new, 2, 4, widths)
     status_clean(m)
     assert tok[:stop].tolist() == plain.tokens[:stop].tolist()
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_padded_batch_stores_nothing_for_its_empty_rows(tree):
+    """A batch of a fixed number of rows of which the last hold no token, in memory that an earlier plan has used."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rows, H, hd, page = 40, 2, 64, 16
+    pool = torch.zeros(8, 2, 1, page, hd, dtype=F16, device="cuda")
+    table, free, rope = torch.full((2, 4), -1, **i32), torch.arange(8, **i32), T.rope_table(64, hd)
+    lens, head = torch.zeros(2, **i32), torch.zeros(1, **i32)
+    x = torch.ones(rows, (H + 2) * hd, dtype=F16, device="cuda")
+    for fresh in ([25, 15], [3, 4], [0, 1], [0, 0]):
+        n = sum(fresh)
+        parents = torch.tensor([-1] * rows, **i32) if tree else None
+        plan = T.plan_batch(lens, torch.tensor(fresh, **i32), table, free, head, page, rows, parents=parents,
+                            mask_words=2 if tree else 0)
+        assert bool((plan.slots[n:] == -1).all()) and bool((plan.positions[n:] == 0).all())
+        assert not tree or bool((plan.masks[n:] == 0).all())
+        st = torch.zeros(1, **i32)
+        before = pool.clone()
+        T.norm_rope_append(x, H, pool, plan.slots, plan.positions, rope, status=st)
+        changed = (pool != before).permute(0, 3, 1, 2, 4).reshape(8 * page, -1).any(1).nonzero()[:, 0].tolist()
+        assert int(st) == 0 and changed == sorted(plan.slots[:n].tolist())
+        lens, head = plan.lens.clone(), plan.free_head.clone()
+        x = x + 1
+        del plan
