@@ -17,12 +17,18 @@
 //
 // Few rows: a cluster of up to 8 CTAs shares a row and its first CTA merges the
 // partial sums and lists over distributed shared memory, with no scratch in
-// global memory and no atomics, so results do not depend on timing.
+// global memory.  Chunks and candidates enter their lists in shared memory in
+// any order (atomic counters) and are then put into a total order, and the sums
+// are joined in a fixed one, so results do not depend on timing.
 //
-// Per lane S and T are fp32 sums of vocab / (256 * CTAs) terms or so, joined
-// in fp32 trees.  Bound by issue as much as by memory: 1000 rows of 131,072 bf16
-// logits with n = 20 take 61 us (4.3 TB/s), without the best 20 53 us (5.0 TB/s);
-// the difference is the end of each row.
+// S and T are held and joined in fp32: a lane adds vocab / (256 * CTAs) terms or
+// so (vocab / 32, 512 at most, where a warp takes a row), then lanes, warps and
+// CTAs meet in trees, and the logarithm is fp32.  That leaves a relative error
+// of a few 2^-24 for ordinary rows and vocab / 256 times 2^-24 at worst, which
+// is a lane's own sum: joining the lanes in fp64 would not lower it.
+// Bound by issue as much as by memory: 1000 rows of 131,072 bf16 logits with
+// n = 20 take 60 us (4.4 TB/s), without the best 20 53 us (5.0 TB/s); the
+// difference is the end of each row.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -372,7 +378,10 @@ __device__ __forceinline__ Part stream_chunks(const T* row, int lead, int V, int
   return p;
 }
 
-// The n-th largest of 32 (n <= 20) or 64 group maxima, two a lane: a bound with n elements at or above it.
+// The n-th largest of 32 (n <= 20) or 64 group maxima, two a lane: a bound with n elements at or above it.  Fewer
+// groups are ordered sooner, but the nearer n is to their number, the more elements reach the bound.  32 against 64
+// groups at n = 20: 62.4 / 63.8 us for 1000 x 131072 bf16, 10.1 / 10.7 for one row of 50,257, but 57 / 53 for 4000 x
+// 16000 (a warp a row); at n = 24 65.1 / 65.2, 10.5 / 10.7 and 63 / 57; at n = 32 90 / 68, 12.9 / 11.5 and 817 / 64.
 __device__ __forceinline__ uint32_t nth_bound(uint32_t g0, uint32_t g1, int n, int lane) {
   if (n <= 20) {
     const uint32_t g = max(g0, g1);
@@ -743,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) logprobs_ker
   for (int i = threadIdx.x; i < n_top; i += kThreads) o.write_top(a, r, i, top[i]);
 }
 
-// A warp a row, for many rows of up to 64 chunks: everything stays in the warp,
+// A warp a row, for many rows of up to 64 chunks and n <= 56: everything stays in the warp,
 // with no barrier.  4000 rows of 8000 bf16 logits, n 20: 37 us, against 60 us
 // with a CTA a row, whose end (several barriers a row) outweighs the row.
 template <class T>
@@ -816,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_warp_kernel(Args a) {
       for (int j = 0; j < n; ++j) rank += cand[j] > k;
       if (rank < n_top) o.write_top(a, r, rank, k);
     }
-  } else {  // many above the bound (ascending values): extract one after another
+  } else {  // many above the bound (ascending values, say): extract one after another, a pass over the row each
     unsigned long long last = ~0ull;
     for (int i = 0; i < n_top; ++i) {
       unsigned long long best = 0;

@@ -13,6 +13,12 @@
 // the problem - and a second, small kernel joins them in order.  No atomics:
 // results do not depend on timing.
 //
+// Every row block of a request runs all of the request's tiles, also where no
+// masks are given and its rows see only a part of the nodes: blocks of prompt
+// positions are right but far from their floor (2 x 4,000 rows from an empty
+// cache, 32 heads over 8, width 128: 1,180 us, floor 161; 8 x 128 rows behind
+// 4,000 positions: 128 us, floor 42).
+//
 // Inside a CTA (flash attention, one pass over the keys with a running maximum
 // and sum per row): a producer warp loads tiles into a ring of stages; four
 // warps multiply, split over the block's 16-row parts and, where those are
@@ -26,7 +32,7 @@
 //
 // Bound by the cache's bytes: a position of a key head is 4 * hd bytes for
 // 4 * hd * BM multiply-adds.  64 single tokens x 32 heads over 8 key heads, 4,000
-// positions of width 128: 174 us, 6.0 TB/s (92 % of a copy), pages of 16 or 64;
+// positions of width 128: 172 us, 6.1 TB/s (93 % of a copy), pages of 16 or 64;
 // 512 such requests of 500 positions: 195 us, 5.4 TB/s (323 us with one CTA of
 // eight multiplying warps an SM).
 #include "tree_attn.h"
@@ -781,7 +787,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeAttnArgs a) {
 }
 
 // Rows of a block: the smallest that holds a request's rows of a key head.  More than 32 rows of widths 64 and 128
-// take the tensor-core kernel's 128.
+// take the tensor-core kernel's 128.  That kernel's tiles are 64 columns (one 128-byte swizzled row) wide, so width 32
+// stays on the warp-level instructions, in blocks of 64 rows: 16 requests x 32 nodes x 4 heads over 8 key heads, 4,000
+// positions, take 58 us (5.6 times the time of their bytes), no less than width 64 on the tensor cores (57 us, 2.8
+// times).
 static int block_rows(int hd, int64_t rows_per_head) {
   if (rows_per_head <= 16) return 16;
   if (rows_per_head <= 32) return 32;

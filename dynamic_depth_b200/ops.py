@@ -53,10 +53,6 @@ def _forward_only():
         raise ValueError("no backward form: detach the tensors or call under torch.no_grad()")
 
 
-def _wants(t):
-    return t is not None and t.requires_grad
-
-
 def _flat(t, dtype, n, name, dev):
     """A contiguous vector of n elements on CUDA device `dev` (None passes as a null pointer)."""
     if t is None:
@@ -172,7 +168,8 @@ def norm_rope_append(qkv, n_heads: int, pool, slots, positions, rope, q_gain=Non
                      q_out=None, status=None) -> torch.Tensor:
     """Per-head RMSNorm (with gains) and rotation of the queries and keys of qkv [rows, (q | k | v) heads * width],
     keys and values stored at `slots` of the pool; returns the queries [rows, n_heads, width] in the pool's type."""
-    if qkv.requires_grad or pool.requires_grad or rope.requires_grad or _wants(q_gain) or _wants(k_gain) or _wants(q_out):
+    if (qkv.requires_grad or pool.requires_grad or rope.requires_grad or q_gain is not None and q_gain.requires_grad
+            or k_gain is not None and k_gain.requires_grad or q_out is not None and q_out.requires_grad):
         _forward_only()
     p = _pool(pool)
     dev, rows, hd = pool.get_device(), qkv.shape[0], p.head_dim
@@ -221,9 +218,9 @@ def tree_attention(q, pool, block_table, ctx_lens, cu, max_nodes: int, masks=Non
                    return_lse: bool = False, workspace=None, status=None):
     """Attention of draft trees over the pool's pages: rows cu[r] .. cu[r+1] of q [rows, heads, width] see request r's
     first ctx_lens[r] positions and the nodes behind them that their mask words name (None: the earlier nodes and
-    themselves).  out: a given tensor's type (the pool's or fp32), else the pool's; it may be q.  Returns out, or
-    (out, lse)."""
-    if q.requires_grad or pool.requires_grad or _wants(out):
+    themselves).  out: a given tensor's type (the pool's or fp32), else the pool's; it may be q.  Rows of no request are
+    left as they are, so in a new tensor undefined.  Returns out, or (out, lse)."""
+    if q.requires_grad or pool.requires_grad or out is not None and out.requires_grad:
         _forward_only()
     p = _pool(pool)
     dev, hd = pool.get_device(), p.head_dim

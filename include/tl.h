@@ -571,7 +571,8 @@ int tl_token_logprobs(const void* dev_logits, int32_t dtype, int64_t rows, int32
  *     on, request after request;  *dev_free_head_out: the next index;
  *   dev_granted [R]: 1 where the request's new tokens have pages.  A request
  *     is granted when it needs no page, or when the list holds the pages that
- *     it and every request before it need; never past max_pages;
+ *     it and every request before it need; never past max_pages (a request that
+ *     would pass it is refused, TL_BAD_LENGTH, and counts as needing none);
  *   dev_lens [R]: cached + fresh where granted, cached elsewhere;
  *   dev_slots [n_rows] int64: page * page_tokens + offset; -1 in a request that
  *     was refused;
@@ -585,8 +586,9 @@ int tl_token_logprobs(const void* dev_logits, int32_t dtype, int64_t rows, int32
  * or NULL masks.  Tokens beyond 32 * mask_words of a request have no bit, their
  * own rows included (TL_BAD_LENGTH).
  * n_rows: rows the row outputs hold; rows from cu[R] on are left as they are,
- * rows past n_rows are not written (TL_BAD_LENGTH).  A negative length, or a
- * dev_fresh above 2^24, counts as 0 and is refused (TL_BAD_LENGTH).
+ * rows past n_rows are not written (TL_BAD_LENGTH).  A negative length, a
+ * dev_fresh above 2^24, or a dev_cached of 2^31 - 2^24 - page_tokens or more
+ * counts as 0 and is refused (TL_BAD_LENGTH).
  * 1 <= R <= 8192; page_tokens a power of two, 1 .. 4096; mask_words 0 .. 8;
  * n_rows <= 2^30, and <= 2^20 with dev_parents;
  * No output (the block table and dev_status among them) shares a byte with an
